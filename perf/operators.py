@@ -214,7 +214,7 @@ def _own(s):
     if case["op"] == "prompt":
         q, k, v = s["qkv"].split([case["Hq"], case["Hkv"], case["Hkv"]], 1)
         return lib.qattn_prompt_attention(q, k, v, s["cu"])
-    cache = lib.PagedKVCache(s["k_codes"], s["v_codes"], s["k_par"], s["v_par"])
+    cache = lib.PagedKVCache(s["k_codes"], s["v_codes"], s["k_par"], s["v_par"], case["bits"])
     if case["op"] == "paged":
         return lib.qattn_paged_attention(s["q"], cache, s["table"], s["cu"], s["kv_len"], max_new=s["most_new"])
     out = {}
