@@ -14,6 +14,10 @@ calls raise.
 `W4A8Linear` wraps the three for a layer; `w4a8_linear_host` is the end to
 end call a user makes with host tensors, and `w4a8_linear_host_many` runs
 several of them with their host copies overlapping the kernels.
+
+attn.py binds the attention operators around the layer (include/qoq_attn.h):
+rotary positions, a paged 4/8-bit key/value cache, attention over it, and
+the attention of whole prompts.
 """
 from __future__ import annotations
 
@@ -24,6 +28,10 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+
+from .attn import (ATTN_SIGNATURES, PagedKVCache, Rotary, paged_kv_cache, qattn_cache_append, qattn_cache_read,  # noqa: F401
+                   qattn_paged_attention, qattn_paged_attention_workspace_bytes, qattn_prompt_attention, qattn_rotary,
+                   rotary_frequencies)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqoq.so")
@@ -94,6 +102,10 @@ def lib() -> ctypes.CDLL:
                     "`python -m w4a8_integer_gemm_b200.build_lib` (there is no CPU fallback)")
             L = ctypes.CDLL(LIB_PATH)
             for name, (res, args) in SIGNATURES.items():
+                f = getattr(L, name)
+                f.restype = res
+                f.argtypes = args
+            for name, (res, args) in ATTN_SIGNATURES.items():
                 f = getattr(L, name)
                 f.restype = res
                 f.argtypes = args
