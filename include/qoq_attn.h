@@ -38,6 +38,8 @@
  *                          cu[b+1] - 1 (n_b rows, maybe none); rows outside
  *                          cu[0] .. cu[B] belong to no sequence, and no call
  *                          writes their outputs.
+ *                          It does not decrease and stays within 0 .. T;
+ *                          a sequence with rows beyond T is not attended.
  *   kv_len  int32 [B]      tokens of sequence b in the cache, its new ones
  *                          included: new token i has position
  *                          kv_len[b] - n_b + i.

@@ -1,0 +1,113 @@
+// qoq_attn_device.cuh -- device code the attention kernels share: which rows
+// a CTA owns, and the expansion of cached codes to FP16.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "qoq_attn_internal.h"
+
+namespace qoq {
+
+struct TileWork {
+    int b;      // sequence, -1: none
+    int row0;   // first row (new token * G + head of the group) of the tile in its sequence
+    int n;      // new tokens of the sequence
+};
+
+struct TileScan {
+    int warp[32];
+    int base, b, row0, n;
+};
+
+// Row tile number `rank` of the batch, counted from the back (the rows that
+// see most come first), over the sequences with lo <= n_b * G <= hi rows:
+// each has ceil(n_b * G / rows) tiles (a sequence with rows outside 0 .. T - 1
+// has none).  The whole CTA takes part; a thread
+// looks at one sequence per pass.
+__device__ __forceinline__ TileWork find_tile(const AttnBatch &a, int T, int G, int rows, int lo, int hi, int rank, TileScan &sc)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (threadIdx.x == 0) {
+        sc.base = 0;
+        sc.b = -1;
+    }
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = a.B - 1 - (b0 + (int)threadIdx.x);
+        int n = 0, tiles = 0;
+        if (b >= 0) {
+            const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
+            n = t0 >= 0 && t1 <= T ? max(0, t1 - t0) : 0;
+            const int64_t r = (int64_t)n * G;
+            tiles = r >= lo && r <= hi ? (int)((r + rows - 1) / rows) : 0;
+        }
+        int x = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();                    // base is up to date, warp[] is free
+        if (lane == 31) sc.warp[warp] = x;
+        __syncthreads();
+        int before = sc.base, total = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) before += sc.warp[w];
+            total += sc.warp[w];
+        }
+        before += x - tiles;
+        if (rank >= before && rank < before + tiles) {
+            sc.b = b;
+            sc.row0 = (tiles - 1 - (rank - before)) * rows;
+            sc.n = n;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) sc.base += total;
+        if (sc.b >= 0) break;
+    }
+    __syncthreads();
+    return {sc.b, sc.row0, sc.n};
+}
+
+__device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// Eight 4-bit codes -> fp16(s c + m) of channels 0 4, 1 5, 2 6, 3 7.  A
+// nibble in bits 0-3 under the exponent of 1024 is 1024 + c, in bits 4-7
+// under that of 64 it is 64 + c (the mantissa's unit is 2^-4 there): one
+// logic operation and one exact subtraction give c, one multiply-add rounds
+// once.  par: (s, m).
+__device__ __forceinline__ uint4 expand4(uint32_t x, uint32_t par)
+{
+    const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
+    const uint32_t y = x >> 8;
+    const uint32_t a = sub_h2((x & 0x000F000Fu) | 0x64006400u, 0x64006400u);
+    const uint32_t b = sub_h2((x & 0x00F000F0u) | 0x54005400u, 0x54005400u);
+    const uint32_t c = sub_h2((y & 0x000F000Fu) | 0x64006400u, 0x64006400u);
+    const uint32_t d = sub_h2((y & 0x00F000F0u) | 0x54005400u, 0x54005400u);
+    return make_uint4(fma_h2(a, s, m), fma_h2(b, s, m), fma_h2(c, s, m), fma_h2(d, s, m));
+}
+
+// Eight 8-bit codes (x: channels 0-3, y: 4-7) -> fp16(s c + m), in order.
+__device__ __forceinline__ uint4 expand8(uint32_t x, uint32_t y, uint32_t par)
+{
+    const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
+    const uint32_t a = sub_h2(__byte_perm(x, 0x64646464u, 0x4140), 0x64006400u);
+    const uint32_t b = sub_h2(__byte_perm(x, 0x64646464u, 0x4342), 0x64006400u);
+    const uint32_t c = sub_h2(__byte_perm(y, 0x64646464u, 0x4140), 0x64006400u);
+    const uint32_t d = sub_h2(__byte_perm(y, 0x64646464u, 0x4342), 0x64006400u);
+    return make_uint4(fma_h2(a, s, m), fma_h2(b, s, m), fma_h2(c, s, m), fma_h2(d, s, m));
+}
+
+}  // namespace qoq

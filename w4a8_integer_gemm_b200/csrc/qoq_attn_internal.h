@@ -65,6 +65,13 @@ size_t paged_attention_workspace(int T, int B, int Hq, int Hkv, int d, int table
 cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                    const AttnBatch &a, int max_new, float scale, uint16_t *out, int64_t ldo,
                                    void *workspace, cudaStream_t stream);
+// Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows; with splits > 1 the
+// keys are shared by that many CTAs, which leave their sums in `part`.
+cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
+                               const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
+                               float *part, cudaStream_t stream);
+// Its error flag (a bounded wait ran out), read and cleared.
+cudaError_t read_and_clear_tile_error(int *value);
 cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream);
