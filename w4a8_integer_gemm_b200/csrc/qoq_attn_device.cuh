@@ -69,6 +69,20 @@ __device__ __forceinline__ TileWork find_tile(const AttnBatch &a, int T, int G, 
     return {sc.b, sc.row0, sc.n};
 }
 
+// The 8 channels of a 16-byte vector in the order the 4-bit codes expand to:
+// 0 4 1 5 2 6 3 7 (the two halves of a code word give a pair).
+__device__ __forceinline__ uint4 to_code_order(uint4 v)
+{
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+__device__ __forceinline__ uint4 from_code_order(uint4 v)
+{
+    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                      __byte_perm(v.z, v.w, 0x7632));
+}
+
 __device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
 {
     uint32_t r;

@@ -70,7 +70,12 @@ cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq
 cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
                                float *part, cudaStream_t stream);
-// Its error flag (a bounded wait ran out), read and cleared.
+// Few rows (qoq_attn_rows.cu): the sequences with at most `few` rows, 8 rows (eight) or 16 to a pass over the cache.
+size_t rows_workspace(int d);
+cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
+                              const AttnBatch &a, int few, bool eight, float scale, uint16_t *out, int64_t ldo,
+                              void *workspace, cudaStream_t stream);
+// The tile kernel's error flag (a bounded wait ran out), read and cleared.
 cudaError_t read_and_clear_tile_error(int *value);
 cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,

@@ -85,20 +85,6 @@ __device__ __forceinline__ uint32_t swz(int row, int vec)
     return (uint32_t)(row * 128 + (((vec & 7) ^ (row & 7)) << 4));
 }
 
-// The 8 channels of a 16-byte vector in the order the 4-bit codes expand to:
-// 0 4 1 5 2 6 3 7 (the two halves of a code word give a pair).
-__device__ __forceinline__ uint4 to_code_order(uint4 v)
-{
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                      __byte_perm(v.y, v.w, 0x7632));
-}
-
-__device__ __forceinline__ uint4 from_code_order(uint4 v)
-{
-    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                      __byte_perm(v.z, v.w, 0x7632));
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
