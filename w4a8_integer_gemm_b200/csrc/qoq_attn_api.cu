@@ -52,6 +52,11 @@ bool valid_paging(int page_size, int pages, int table_pages)
            table_pages >= 1 && (int64_t)table_pages * page_size <= kMaxTokens;
 }
 
+int page_shift(int page_size)
+{
+    return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+}
+
 bool valid_rotary(const double *freq, int d, int rot, int interleaved, float amplitude)
 {
     if (rot < 0 || rot > d || rot % 16 != 0 || (interleaved != 0 && interleaved != 1)) return false;
@@ -106,7 +111,7 @@ int qattn_cache_append(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_
     return from_cuda(qoq::launch_cache_append(k, ldk, v, ldv, q, ldq, q_out, ldqo, T, q ? Hq : 0, Hkv, d,
                                               {freq, rot, interleaved, amplitude},
                                               {k_codes, v_codes, k_par, v_par, bits},
-                                              {cu, kv_len, table, B, table_pages, page_size, pages},
+                                              {cu, kv_len, table, B, table_pages, page_size, pages, page_shift(page_size)},
                                               (cudaStream_t)stream));
 }
 
@@ -125,7 +130,7 @@ int qattn_cache_read(const uint8_t *k_codes, const uint8_t *v_codes, const uint1
     return from_cuda(qoq::launch_cache_read(
         {const_cast<uint8_t *>(k_codes), const_cast<uint8_t *>(v_codes), const_cast<uint16_t *>(k_par),
          const_cast<uint16_t *>(v_par), bits},
-        {cu, kv_len, table, B, table_pages, page_size, pages}, T, Hkv, d, K, V, (cudaStream_t)stream));
+        {cu, kv_len, table, B, table_pages, page_size, pages, page_shift(page_size)}, T, Hkv, d, K, V, (cudaStream_t)stream));
 }
 
 size_t qattn_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size,
@@ -159,7 +164,7 @@ int qattn_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv
         q, ldq, T, Hq, Hkv, d,
         {const_cast<uint8_t *>(k_codes), const_cast<uint8_t *>(v_codes), const_cast<uint16_t *>(k_par),
          const_cast<uint16_t *>(v_par), bits},
-        {cu, kv_len, table, B, table_pages, page_size, pages}, max_new, scale, out, ldo, workspace,
+        {cu, kv_len, table, B, table_pages, page_size, pages, page_shift(page_size)}, max_new, scale, out, ldo, workspace,
         (cudaStream_t)stream));
 }
 
@@ -175,7 +180,7 @@ int qattn_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, in
     const int dev = check_device();
     if (dev != QOQ_OK) return dev;
     return from_cuda(qoq::launch_prompt_attention(q, ldq, k, ldk, v, ldv, T, Hq, Hkv, d,
-                                                  {cu, nullptr, nullptr, B, 0, 0, 0}, scale, out, ldo,
+                                                  {cu, nullptr, nullptr, B, 0, 0, 0, 0}, scale, out, ldo,
                                                   (cudaStream_t)stream));
 }
 

@@ -15,6 +15,7 @@ struct AttnBatch {
     const int32_t *kv_len;   // [B]; null for prompts
     const int32_t *table;    // [B][table_pages]; null for prompts
     int B, table_pages, page_size, pages;
+    int page_shift;          // page_size == 1 << page_shift
 };
 
 struct AttnCache {
@@ -47,7 +48,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ cu, int B
 __device__ __forceinline__ int page_of(const AttnBatch &a, int b, int pos)
 {
     if (pos < 0) return -1;
-    const int p = pos / a.page_size;
+    const int p = pos >> a.page_shift;
     if (p >= a.table_pages) return -1;
     const int page = __ldg(a.table + (size_t)b * a.table_pages + p);
     return page >= 0 && page < a.pages ? page : -1;

@@ -23,15 +23,19 @@
 //
 // Running maximum m, sum l and sum of p m' in FP32; m may lag behind by 2^8,
 // so O is rescaled rarely.  The weights p s are rounded to FP16 (half a step
-// each); they are scaled by a power of two per row, k, that follows their
-// own maximum, so that small scales do not underflow.
+// each) after a power of two k, which follows the largest s, so that small
+// scales do not underflow.
 //
-// Work: items of 256 tokens of a (sequence, row tile, KV head), in that
-// order; CTA c of P takes items c I / P .. (c + 1) I / P - 1, so all CTAs
-// read the same number of bytes whatever the lengths.  A run of items of one
-// (sequence, row tile, head) that lies within a CTA is finished there; one
-// that spans CTAs leaves a partial result in each and a second kernel joins
-// them, in order.
+// Work: a run is a (sequence, row tile, KV head) with its tokens in granules
+// of 16, in that order; each run also counts kSwitch granules for what it
+// costs to begin and end one.  Warp w of P takes an equal, contiguous share
+// of that line, so all warps do the same work whatever the lengths, and
+// neither a barrier nor shared memory ties them.  A run within one warp's
+// share is finished there; one that spans warps leaves a partial result in
+// each, and a second kernel joins them, in order.  (An earlier form shared
+// each run among the eight warps of a CTA and merged them in shared memory:
+// 122 against XXX us for 64 sequences of 300 to 8191 tokens, because CTAs
+// with short runs spent their time switching.)
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -48,7 +52,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kItem = 256;              // tokens of an item
+constexpr int kSwitch = 2;              // granules that a run counts for its beginning and end
+constexpr int kLeast = 4;               // granules of a warp's share, at least (a partial result costs about as much)
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct RowsArgs {
@@ -60,8 +65,10 @@ struct RowsArgs {
     int T, Hq, Hkv, G;
     int few;            // sequences with more rows are another kernel's
     float scale_log2;   // scale * log2(e)
-    float *part;        // [P][2][rows][D + 2]
-    int4 *joined;       // [P]: (sequence or -1, first row, KV head, first CTA) of the run that ends in CTA c's first part
+    uint32_t e6, e5;    // 0x64006400, 0x54005400: see pair_lo
+    float *part;        // [P][2][rows][D + 4]: sums, maximum, sum of weights
+    int4 *joined;       // [P]: (sequence or -1, first row, KV head, first warp) of the run that ends in warp w's share
+                        // and began in an earlier one's
 };
 
 // D (16 x 8, FP32) += A (16 x 16, FP16, row) * B (16 x 8, FP16, col).
@@ -88,26 +95,28 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// (code - off) pairs of a word: 4 bits: nibbles (0, 4) and (1, 5) of the 16-bit halves' low bytes
-__device__ __forceinline__ uint32_t pair_lo(uint32_t x)
+// (code - off) pairs of a word: 4 bits: nibbles (0, 4) and (1, 5) of the 16-bit halves' low bytes.  The exponent
+// patterns e6 = 0x64006400 and e5 = 0x54005400 come in registers whose values the compiler does not know: a logic
+// instruction has room for one constant, and with two it becomes two (a quarter of this kernel's instructions).
+__device__ __forceinline__ uint32_t pair_lo(uint32_t x, uint32_t e6)
 {
-    return sub_h2((x & 0x000F000Fu) | 0x64006400u, 0x64086408u);   // 1024 + c - 1032
+    return sub_h2((x & 0x000F000Fu) | e6, 0x64086408u);   // 1024 + c - 1032
 }
 
-__device__ __forceinline__ uint32_t pair_hi(uint32_t x)
+__device__ __forceinline__ uint32_t pair_hi(uint32_t x, uint32_t e5)
 {
-    return sub_h2((x & 0x00F000F0u) | 0x54005400u, 0x54805480u);   // 64 + c - 72
+    return sub_h2((x & 0x00F000F0u) | e5, 0x54805480u);   // 64 + c - 72
 }
 
 // 8 bits: bytes (0, 1) or (2, 3) of x
-__device__ __forceinline__ uint32_t bytes_lo(uint32_t x)
+__device__ __forceinline__ uint32_t bytes_lo(uint32_t x, uint32_t e6)
 {
-    return sub_h2(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
+    return sub_h2(__byte_perm(x, e6, 0x5150), 0x64806480u);
 }
 
-__device__ __forceinline__ uint32_t bytes_hi(uint32_t x)
+__device__ __forceinline__ uint32_t bytes_hi(uint32_t x, uint32_t e6)
 {
-    return sub_h2(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
+    return sub_h2(__byte_perm(x, e6, 0x5352), 0x64806480u);
 }
 
 template <int N>
@@ -134,104 +143,102 @@ struct RowsCfg {
     static constexpr int kKW = kRowBytes / 16;            // words of a key per lane
     static constexpr int kVW = kRowBytes / 32;            // words of a value per lane
     static constexpr int kMt = D / 16;                    // 16-channel tiles of O^T
-    static constexpr int kGr = BITS == 8 && D == 128 ? 1 : 2;   // 16-token granules per group (registers bound it)
+    static constexpr int kGr = D == 128 ? 1 : 2;   // 16-token granules per group (registers bound it)
+    static constexpr int kGroup = 16 * kGr;               // tokens
     static constexpr int kRows = 8 * NT;
-    static constexpr int kStride = D + 4;                 // floats of a row in the merge buffer
-    static constexpr int kSmem = kWarps * kRows * kStride * 4;
+    static constexpr int kStride = D + 4;                 // floats of a partial row
     static constexpr float kOff = BITS == 4 ? 8.0f : 128.0f;
 };
 
-struct Run {            // a run of items in one (sequence, row tile, head)
-    int b, n, row0, hk, chunk0, chunks;
+struct Run {
+    int b, n, row0, hk, grains;
 };
 
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(const RowsArgs p)
 {
     using C = RowsCfg<D, BITS, NT>;
-    extern __shared__ __align__(16) float merge[];       // [kWarps][rows][kStride]
-    __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-    __shared__ long long s_scan[kWarps];
-    __shared__ long long s_skip;
-    __shared__ int s_b;
+    __shared__ long long s_sum[kWarps], s_before[kThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const AttnBatch &a = p.a;
     const int capacity = a.table_pages * a.page_size;
+    const uint32_t e6 = p.e6, e5 = p.e5;
+    // neighbouring warps of the line sit on different SMs, so that a short line uses all of them
+    const int me = warp * gridDim.x + blockIdx.x;
 
-    // items of sequence b; n and chunks are set
-    auto items_of = [&](int b, int &n, int &chunks) -> long long {
+    // the line's length over sequence b; n and grains are set
+    auto length_of = [&](int b, int &n, int &grains) -> long long {
         const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
         n = t0 >= 0 && t1 <= p.T ? max(0, t1 - t0) : 0;
         if ((long long)n * p.G > p.few) n = 0;
-        const int len = max(1, min(__ldg(a.kv_len + b), capacity));
-        chunks = (len + kItem - 1) / kItem;
-        return (long long)((n * p.G + C::kRows - 1) / C::kRows) * p.Hkv * chunks;
+        grains = (max(1, min(__ldg(a.kv_len + b), capacity)) + 15) / 16;
+        return (long long)((n * p.G + C::kRows - 1) / C::kRows) * p.Hkv * (grains + kSwitch);
     };
 
-    // ---- this CTA's items ----
-    long long at, end;
+    // ---- this warp's share ----
+    long long at, end, total, ctas;
     Run run;
     {
         const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
         long long mine = 0;
-        int n, chunks;
-        for (int b = b0; b < b1; ++b) mine += items_of(b, n, chunks);
+        for (int b = b0; b < b1; ++b) mine += length_of(b, run.n, run.grains);
         long long x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) s_scan[warp] = x;
+        if (lane == 31) s_sum[warp] = x;
         __syncthreads();
-        long long before = x - mine, total = 0;
+        total = 0;
+        x -= mine;
         for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s_scan[w];
-            total += s_scan[w];
+            if (w < warp) x += s_sum[w];
+            total += s_sum[w];
         }
-        // no more CTAs than items: every CTA between a run's first and last one has a part of it
-        const long long ctas = min((long long)gridDim.x, total);
-        at = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-        end = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
-        if (at < end && at >= before && at < before + mine) {
-            int b = b0;
-            for (; b < b1; ++b) {
-                const long long k = items_of(b, n, chunks);
-                if (at < before + k) break;
-                before += k;
-            }
-            s_b = b;
-            s_skip = at - before;
-        }
-        if (threadIdx.x == 0) p.joined[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        s_before[threadIdx.x] = x;
+        if (lane == 0) p.joined[me] = make_int4(-1, 0, 0, 0);
         __syncthreads();
         grid_launch_dependents();
-        if (at >= end) return;
-        run.b = s_b;
-        items_of(run.b, run.n, run.chunks);
-        const long long skip = s_skip;
-        run.chunk0 = (int)(skip % run.chunks);
-        run.hk = (int)(skip / run.chunks % p.Hkv);
-        run.row0 = (int)(skip / run.chunks / p.Hkv) * C::kRows;
-        // total is needed below for the first CTA of a run
-        s_scan[0] = total;    // every thread has read s_scan; the next read is after a barrier
+        ctas = min((long long)gridDim.x * kWarps, (total + kLeast - 1) / kLeast);
+        if (me >= ctas) return;
+        at = total * me / ctas;
+        end = total * (me + 1) / ctas;
+        int lo = 0, hi = kThreads - 1;               // the last thread whose sequences begin at or before `at`
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_before[mid] <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        long long skip = at - s_before[lo];
+        for (run.b = lo * per;; ++run.b) {
+            const long long len = length_of(run.b, run.n, run.grains);
+            if (skip < len) break;
+            skip -= len;
+        }
+        const int unit = run.grains + kSwitch;
+        const int r = (int)(skip / unit);
+        run.hk = r % p.Hkv;
+        run.row0 = r / p.Hkv * C::kRows;
+        at -= skip % unit;                           // where the run begins; the share begins within it
     }
-    bool head = true;         // the CTA's first run
+    long long from = total * me / ctas;              // where the warp's part of the run begins
 
     while (at < end) {
         const int b = run.b, hk = run.hk, rows = run.n * p.G - run.row0;
-        const int take = (int)min((long long)(run.chunks - run.chunk0), end - at);
+        // granules [g0, g1) of the run
+        const int g0 = (int)max(0ll, from - at - kSwitch), g1 = (int)min((long long)run.grains, end - at - kSwitch);
+        if (g0 < g1) {
         const int len = min(__ldg(a.kv_len + b), capacity), first = __ldg(a.kv_len + b) - run.n;
         const int t_seq = __ldg(a.cu + b);
-        // the warp's tokens: an equal, contiguous share
-        const int tok0 = run.chunk0 * kItem + warp * take * (kItem / kWarps);
-        const int tok1 = min(tok0 + take * (kItem / kWarps), len);
+        const int tok0 = 16 * g0, tok1 = min(16 * g1, len);
 
         // ---- q fragments, sums, limits of the lane's columns ----
         uint32_t qf[NT][D / 16][2];
-        float sq[NT][2], m[NT][2], l[NT][2], W[NT][2], k[NT][2];
-        int see[NT][2];
+        float sq[NT][2], m[NT][2], l[NT][2], W[NT][2];
+        float k = 0.0f;                                  // power of two on the value scales; 0: none seen yet
+        int see[NT][2], see_max = 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int row = 8 * t + g;
@@ -274,14 +281,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 const int col = 8 * t + 2 * c + u;
                 sq[t][u] = __shfl_sync(0xffffffffu, s, (2 * c + u) * 4) * p.scale_log2;
                 see[t][u] = col < rows ? first + (run.row0 + col) / p.G + 1 : 0;
+                see_max = max(see_max, see[t][u]);
                 m[t][u] = -INFINITY;
-                l[t][u] = W[t][u] = k[t][u] = 0.0f;
+                l[t][u] = W[t][u] = 0.0f;
             }
         }
         int see_min = see[0][0];
 #pragma unroll
         for (int t = 0; t < NT; ++t) see_min = min(see_min, min(see[t][0], see[t][1]));
         see_min = __reduce_min_sync(0xffffffffu, see_min);
+        see_max = __reduce_max_sync(0xffffffffu, see_max);
 
         float o[NT][C::kMt][4];
 #pragma unroll
@@ -302,16 +311,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 bs[i] = page < 0 ? kNone : ((uint32_t)page * p.Hkv + hk) * a.page_size + (pos & (a.page_size - 1));
             }
         };
+        // a lane's place in a granule: keys g and g + 8, values 2c, 2c + 1, 2c + 8, 2c + 9
+        const uint8_t *kc0 = p.c.k_codes + g * C::kRowBytes + (C::kKW >= 4 ? 16 : 4 * C::kKW) * c;
+        const uint8_t *vc0 = p.c.v_codes + 2 * c * C::kRowBytes + 4 * C::kVW * g;
+        const uint32_t *kp0 = reinterpret_cast<const uint32_t *>(p.c.k_par) + g;
+        const uint32_t *vp0 = reinterpret_cast<const uint32_t *>(p.c.v_par) + g;
         auto load_k = [&](const uint32_t (&bs)[C::kGr]) {
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
                 if (bs[i] == kNone) continue;
-                const uint8_t *src = p.c.k_codes + (size_t)(bs[i] + g) * C::kRowBytes + (C::kKW >= 4 ? 16 : 4 * C::kKW) * c;
+                const uint8_t *src = kc0 + (size_t)bs[i] * C::kRowBytes;
+                const uint32_t *par = kp0 + bs[i];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     load_words<C::kKW < 4 ? C::kKW : 4>(src + 8 * h * C::kRowBytes, kw[i][h]);
                     if (C::kKW == 8) load_words<4>(src + 8 * h * C::kRowBytes + 64, kw[i][h] + (C::kKW == 8 ? 4 : 0));
-                    kp[i][h] = __ldg(reinterpret_cast<const uint32_t *>(p.c.k_par) + bs[i] + g + 8 * h);
+                    kp[i][h] = __ldg(par + 8 * h);
                 }
             }
         };
@@ -319,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
                 if (bs[i] == kNone) continue;
-                const uint8_t *src = p.c.v_codes + (size_t)(bs[i] + 2 * c) * C::kRowBytes + 4 * C::kVW * g;
+                const uint8_t *src = vc0 + (size_t)bs[i] * C::kRowBytes;
+                const uint32_t *par = vp0 + bs[i];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) load_words<C::kVW>(src + ((u & 1) + 8 * (u >> 1)) * C::kRowBytes, vw[i][u]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    vp[i][h] = __ldg(reinterpret_cast<const uint32_t *>(p.c.v_par) + bs[i] + g + 8 * h);
+                for (int h = 0; h < 2; ++h) vp[i][h] = __ldg(par + 8 * h);
             }
         };
         locate(tok0, base);
@@ -346,20 +361,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     uint32_t a0, a1, a2, a3;
                     if (BITS == 4) {
                         const uint32_t x = kw[i][0][j / 2] >> (8 * (j & 1)), y = kw[i][1][j / 2] >> (8 * (j & 1));
-                        a0 = pair_lo(x);
-                        a1 = pair_lo(y);
-                        a2 = pair_hi(x);
-                        a3 = pair_hi(y);
+                        a0 = pair_lo(x, e6);
+                        a1 = pair_lo(y, e6);
+                        a2 = pair_hi(x, e5);
+                        a3 = pair_hi(y, e5);
                     } else {
                         const uint32_t x = kw[i][0][j % C::kKW], y = kw[i][1][j % C::kKW];
-                        a0 = bytes_lo(x);
-                        a1 = bytes_lo(y);
-                        a2 = bytes_hi(x);
-                        a3 = bytes_hi(y);
+                        a0 = bytes_lo(x, e6);
+                        a1 = bytes_lo(y, e6);
+                        a2 = bytes_hi(x, e6);
+                        a3 = bytes_hi(y, e6);
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma16816(sc[i][t], a0, a1, a2, a3, qf[t][j][0], qf[t][j][1]);
                 }
+            }
+            // Tokens that no row sees may hold anything: their parameters become zeros, so that nothing below is NaN.
+            const bool edge = tok + C::kGroup > see_min || base[0] == kNone || base[C::kGr - 1] == kNone;
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < C::kGr; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (base[i] == kNone || tok + 16 * i + g + 8 * h >= see_max) kp[i][h] = vp[i][h] = 0u;
             }
             float top[NT][2];
 #pragma unroll
@@ -373,17 +397,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     km[h] = fmaf(C::kOff, s, half_bits_to_float((uint16_t)(kp[i][h] >> 16)));
                     ks[h] = s * p.scale_log2;
                 }
-                const bool edge = base[i] == kNone || tok + 16 * i + 16 > see_min;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float x = fmaf(sc[i][t][r], ks[r >> 1], km[r >> 1] * sq[t][r & 1]);
-                        if (edge && (base[i] == kNone || tok + 16 * i + g + 8 * (r >> 1) >= see[t][r & 1])) x = -INFINITY;
-                        sc[i][t][r] = x;
-                        top[t][r & 1] = fmaxf(top[t][r & 1], x);
-                    }
+                    for (int r = 0; r < 4; ++r) sc[i][t][r] = fmaf(sc[i][t][r], ks[r >> 1], km[r >> 1] * sq[t][r & 1]);
             }
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < C::kGr; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (base[i] == kNone || tok + 16 * i + g + 8 * (r >> 1) >= see[t][r & 1]) sc[i][t][r] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < C::kGr; ++i)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) top[t][r & 1] = fmaxf(top[t][r & 1], sc[i][t][r]);
             // the key registers are free: the next group's
             load_k(base1);
             bool grow = false;
@@ -412,55 +445,49 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                         }
                     }
             }
-            // weights: sc becomes p s k, top its maximum
+            // value scales; k brings the largest seen into [2^5, 2^6), so that with p <= 2^8 the products fit FP16
+            // and scales down to 2^-20 of the largest keep full precision
+            float vs[C::kGr][2], vm[C::kGr][2], vmax = 0.0f;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C::kGr; ++i) {
-                float vs[2], vm[2];
+            for (int i = 0; i < C::kGr; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    vs[h] = half_bits_to_float((uint16_t)(vp[i][h] & 0xFFFFu));
-                    vm[h] = fmaf(C::kOff, vs[h], half_bits_to_float((uint16_t)(vp[i][h] >> 16)));
+                    vs[i][h] = half_bits_to_float((uint16_t)(vp[i][h] & 0xFFFFu));
+                    vm[i][h] = fmaf(C::kOff, vs[i][h], half_bits_to_float((uint16_t)(vp[i][h] >> 16)));
+                    vmax = fmaxf(vmax, vs[i][h]);
                 }
+            if (__any_sync(0xffffffffu, k == 0.0f ? vmax > 0.0f : vmax * k >= 64.0f)) {
+                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 4));
+                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 8));
+                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 16));
+                // vmax in [2^e, 2^(e+1)) (an FP16 number, normal in FP32): k = 2^(5-e)
+                const float k1 = __uint_as_float((127u + 5u + 127u - (__float_as_uint(vmax) >> 23)) << 23);
+                const float f = k1 / (k == 0.0f ? k1 : k);
+                k = k1;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[t][mt][r] *= f;
+            }
+            // weights: sc becomes p s k
+            float sub[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) sub[t][u] = m[t][u] == -INFINITY ? 0.0f : m[t][u];
+#pragma unroll
+            for (int i = 0; i < C::kGr; ++i) {
+                const float vk[2] = {vs[i][0] * k, vs[i][1] * k};
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float x = sc[i][t][r];
-                        const float w = x == -INFINITY ? 0.0f : exp2_fast(x - m[t][r & 1]);
+                        const float w = exp2_fast(sc[i][t][r] - sub[t][r & 1]);
                         l[t][r & 1] += w;
-                        // (an unseen token's parameters may be anything)
-                        W[t][r & 1] = w > 0.0f ? fmaf(w, vm[r >> 1], W[t][r & 1]) : W[t][r & 1];
-                        sc[i][t][r] = w > 0.0f ? w * vs[r >> 1] : 0.0f;
-                        top[t][r & 1] = fmaxf(top[t][r & 1], sc[i][t][r]);
-                    }
-            }
-            bool over = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) over |= k[t][u] == 0.0f ? top[t][u] > 0.0f : top[t][u] * k[t][u] > 16384.0f;
-            if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float x = top[t][u];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        // 2^-e for x in [2^e, 2^(e+1)), e held within 2^-100 .. 2^100; only ever downwards
-                        const int e = min(max((int)(__float_as_uint(x) >> 23) - 127, -100), 100);
-                        const float k1 = __uint_as_float((uint32_t)(127 - e) << 23);
-                        const bool set = x > 0.0f && (k[t][u] == 0.0f || k1 < k[t][u]);
-                        const float f = set && k[t][u] > 0.0f ? k1 / k[t][u] : 1.0f;
-                        if (set) k[t][u] = k1;
-#pragma unroll
-                        for (int mt = 0; mt < C::kMt; ++mt) {
-                            o[t][mt][u] *= f;
-                            o[t][mt][2 + u] *= f;
-                        }
+                        W[t][r & 1] = fmaf(w, vm[i][r >> 1], W[t][r & 1]);
+                        sc[i][t][r] = w * vk[r >> 1];
                     }
             }
 #pragma unroll
@@ -471,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const __half2 x = __floats2half2_rn(sc[i][t][2 * h] * k[t][0], sc[i][t][2 * h + 1] * k[t][1]);
+                        const __half2 x = __floats2half2_rn(sc[i][t][2 * h], sc[i][t][2 * h + 1]);
                         pb[t][h] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
                     }
                 auto tile = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -486,15 +513,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                             // bytes 2h, 2h + 1 of one token under those of the next
                             const uint32_t x = __byte_perm(vw[i][0][w], vw[i][1][w], h ? 0x7632 : 0x5410);
                             const uint32_t y = __byte_perm(vw[i][2][w], vw[i][3][w], h ? 0x7632 : 0x5410);
-                            tile(4 * w + 2 * h, pair_lo(x), pair_hi(x), pair_lo(y), pair_hi(y));
-                            tile(4 * w + 2 * h + 1, pair_lo(x >> 8), pair_hi(x >> 8), pair_lo(y >> 8), pair_hi(y >> 8));
+                            tile(4 * w + 2 * h, pair_lo(x, e6), pair_hi(x, e5), pair_lo(y, e6), pair_hi(y, e5));
+                            tile(4 * w + 2 * h + 1, pair_lo(x >> 8, e6), pair_hi(x >> 8, e5), pair_lo(y >> 8, e6), pair_hi(y >> 8, e5));
                         }
                     } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t x = __byte_perm(vw[i][0][w], vw[i][1][w], h ? 0x7362 : 0x5140);
                             const uint32_t y = __byte_perm(vw[i][2][w], vw[i][3][w], h ? 0x7362 : 0x5140);
-                            tile(2 * w + h, bytes_lo(x), bytes_hi(x), bytes_lo(y), bytes_hi(y));
+                            tile(2 * w + h, bytes_lo(x, e6), bytes_hi(x, e6), bytes_lo(y, e6), bytes_hi(y, e6));
                         }
                     }
                 }
@@ -505,81 +532,62 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             locate(tok + 32 * C::kGr, base1);
         }
 
-        // ---- merge the warps ----
+        // ---- finish, or leave a partial result ----
+        const bool begins = g0 == 0, ends = g1 == run.grains;
+        // a part that began in an earlier warp's share is the warp's first (slot 0), one that goes on its last
+        float *part = p.part + ((size_t)me * 2 + (begins ? 1 : 0)) * C::kRows * C::kStride;
+        const float inv_k = k > 0.0f ? 1.0f / k : 0.0f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float x = l[t][u], y = W[t][u];
 #pragma unroll
-                for (int sft = 4; sft < 32; sft <<= 1) {
-                    x += __shfl_xor_sync(0xffffffffu, x, sft);
-                    y += __shfl_xor_sync(0xffffffffu, y, sft);
+                for (int w = 4; w < 32; w <<= 1) {
+                    x += __shfl_xor_sync(0xffffffffu, x, w);
+                    y += __shfl_xor_sync(0xffffffffu, y, w);
                 }
-                l[t][u] = x;
-                W[t][u] = y;
-                if (g == 0) {
-                    s_m[warp][8 * t + 2 * c + u] = m[t][u];
-                    s_l[warp][8 * t + 2 * c + u] = x;
-                }
-            }
-        __syncthreads();
-        const long long total = s_scan[0];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
                 const int col = 8 * t + 2 * c + u;
-                float M = -INFINITY;
+                if (col >= rows) continue;
+                // the lane's channels: D / 8 * g + 2 mt, + 1
+                float v[2 * C::kMt];
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][col]);
-                const float f = m[t][u] == -INFINITY ? 0.0f : exp2_fast(m[t][u] - M);
-                const float fk = k[t][u] > 0.0f ? f / k[t][u] : 0.0f, fw = f * W[t][u];
-                float *dst = merge + (warp * C::kRows + col) * C::kStride;
+                for (int mt = 0; mt < C::kMt; ++mt) {
+                    v[2 * mt] = fmaf(o[t][mt][u], inv_k, y);
+                    v[2 * mt + 1] = fmaf(o[t][mt][2 + u], inv_k, y);
+                }
+                if (begins && ends) {
+                    const float inv = x > 0.0f ? 1.0f / x : 0.0f;
+                    const int r = run.row0 + col;
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo +
+                                                           (size_t)(hk * p.G + r % p.G) * D + (D / 8) * g);
 #pragma unroll
-                for (int mt = 0; mt < C::kMt; ++mt)
-                    *reinterpret_cast<float2 *>(dst + 16 * mt + 2 * g) =
-                        make_float2(fmaf(o[t][mt][u], fk, fw), fmaf(o[t][mt][2 + u], fk, fw));
+                    for (int i = 0; i < C::kMt / 4; ++i) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __half2 z = __floats2half2_rn(v[8 * i + 2 * e] * inv, v[8 * i + 2 * e + 1] * inv);
+                            h[e] = *reinterpret_cast<const uint32_t *>(&z);
+                        }
+                        dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                } else {
+                    float *dst = part + col * C::kStride;
+#pragma unroll
+                    for (int i = 0; i < C::kMt / 2; ++i)
+                        reinterpret_cast<float4 *>(dst + (D / 8) * g)[i] =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    if (g == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(m[t][u], x);
+                }
             }
-        __syncthreads();
-        const bool whole = run.chunk0 == 0 && take == run.chunks;
-        // a run that began in an earlier CTA is the CTA's first part, one that goes on in a later one its last
-        float *part = p.part + ((size_t)blockIdx.x * 2 + (run.chunk0 > 0 ? 0 : 1)) * C::kRows * (D + 2);
-        for (int e = threadIdx.x; e < C::kRows * (D / 2); e += kThreads) {
-            const int col = e / (D / 2), x = e % (D / 2);             // the pair at 16 mt + 2 g: x = 8 mt + g
-            if (col >= rows) continue;
-            float M = -INFINITY, L = 0.0f, s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][col]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 y = *reinterpret_cast<const float2 *>(merge + (w * C::kRows + col) * C::kStride + 2 * x);
-                s0 += y.x;
-                s1 += y.y;
-                L += s_m[w][col] == -INFINITY ? 0.0f : s_l[w][col] * exp2_fast(s_m[w][col] - M);
-            }
-            const int ch = (D / 8) * (x % 8) + 2 * (x / 8);
-            if (whole) {
-                const int r = run.row0 + col;
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                const __half2 h = __floats2half2_rn(s0 * inv, s1 * inv);
-                *reinterpret_cast<__half2 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(hk * p.G + r % p.G) * D + ch) = h;
-            } else {
-                *reinterpret_cast<float2 *>(part + col * (D + 2) + ch) = make_float2(s0, s1);
-                if (x == 0) *reinterpret_cast<float2 *>(part + col * (D + 2) + D) = make_float2(M, L);
-            }
+        // the warp whose share holds the run's first granule
+        if (lane == 0 && ends && !begins)
+            p.joined[me] = make_int4(b, run.row0, hk, (int)(((at + kSwitch + 1) * ctas - 1) / total));
         }
-        if (threadIdx.x == 0 && head && run.chunk0 > 0 && run.chunk0 + take == run.chunks) {
-            // the run that ends here began at item at - chunk0
-            const long long i0 = at - run.chunk0;
-            p.joined[blockIdx.x] = make_int4(b, run.row0, hk, (int)(((i0 + 1) * min((long long)gridDim.x, total) - 1) / total));
-        }
-        __syncthreads();
         // ---- the next run ----
-        head = false;
-        at += take;
+        at += run.grains + kSwitch;
+        from = at;
         if (at < end) {
-            run.chunk0 = 0;
             if (++run.hk == p.Hkv) {
                 run.hk = 0;
                 run.row0 += C::kRows;
@@ -587,41 +595,81 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     run.row0 = 0;
                     do {
                         ++run.b;
-                    } while (items_of(run.b, run.n, run.chunks) == 0);
+                    } while (length_of(run.b, run.n, run.grains) == 0);
                 }
             }
         }
     }
 }
 
-// One CTA per CTA of the first kernel: joins the run that ended in its first
-// part.  A thread takes channels, the parts in order.
+// One CTA per warp of the first kernel: joins the run that ended in its
+// share.  Its warps take every eighth part, a lane four channels of all rows;
+// the warps' sums are joined in order.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) attn_rows_join_kernel(const RowsArgs p)
+__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs p)
 {
-    constexpr int kRows = 8 * NT;
+    constexpr int kRows = 8 * NT, kStride = D + 4;
+    __shared__ float4 s_v[kWarps][8][D / 4];
+    __shared__ float2 s_ml[kWarps][8];
     grid_dependency_wait();
     const int4 j = p.joined[blockIdx.x];
     if (j.x < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t_seq = __ldg(p.a.cu + j.x), n = __ldg(p.a.cu + j.x + 1) - t_seq, rows = min(kRows, n * p.G - j.y);
-    const int ch = threadIdx.x;
-    for (int col = blockIdx.y; col < rows; col += gridDim.y) {
-        auto part = [&](int cta) {
-            return p.part + (((size_t)cta * 2 + (cta == j.w ? 1 : 0)) * kRows + col) * (D + 2);
-        };
-        float M = -INFINITY, L = 0.0f, s = 0.0f;
-        for (int cta = j.w; cta <= (int)blockIdx.x; ++cta) {
-            const float *x = part(cta);
-            const float m = x[D], l = x[D + 1], v = x[ch];
-            if (m == -INFINITY) continue;
-            const float m1 = fmaxf(M, m), f0 = M == -INFINITY ? 0.0f : exp2_fast(M - m1), f1 = exp2_fast(m - m1);
-            M = m1;
-            L = fmaf(L, f0, l * f1);
-            s = fmaf(s, f0, v * f1);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        float4 v[8];
+        float M[8], L[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            M[i] = -INFINITY;
+            L[i] = 0.0f;
         }
-        const int r = j.y + col;
-        p.out[(int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + ch] =
-            float_to_half_bits(L > 0.0f ? s / L : 0.0f);
+        for (int w = j.w + warp; w <= (int)blockIdx.x; w += kWarps) {
+            const float *part = p.part + ((size_t)w * 2 + (w == j.w ? 1 : 0)) * kRows * kStride;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (r0 + i >= rows) break;
+                const float *x = part + (r0 + i) * kStride;
+                const float2 ml = *reinterpret_cast<const float2 *>(x + D);
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (lane < D / 4) y = *reinterpret_cast<const float4 *>(x + 4 * lane);
+                const float m1 = fmaxf(M[i], ml.x);
+                const float f0 = M[i] == -INFINITY ? 0.0f : exp2_fast(M[i] - m1), f1 = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m1);
+                M[i] = m1;
+                L[i] = fmaf(L[i], f0, ml.y * f1);
+                v[i] = make_float4(fmaf(v[i].x, f0, y.x * f1), fmaf(v[i].y, f0, y.y * f1), fmaf(v[i].z, f0, y.z * f1),
+                                   fmaf(v[i].w, f0, y.w * f1));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (lane < D / 4) s_v[warp][i][lane] = v[i];
+            if (lane == 0) s_ml[warp][i] = make_float2(M[i], L[i]);
+        }
+        __syncthreads();
+        // warp i finishes row i
+        if (r0 + warp < rows && lane < D / 4) {
+            float m = -INFINITY, l = 0.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][warp].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = s_ml[w][warp];
+                const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m);
+                const float4 y = s_v[w][warp][lane];
+                l = fmaf(ml.y, f, l);
+                x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+            }
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int r = j.y + r0 + warp;
+            const __half2 h0 = __floats2half2_rn(x.x * inv, x.y * inv), h1 = __floats2half2_rn(x.z * inv, x.w * inv);
+            *reinterpret_cast<uint2 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + 4 * lane) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+        }
+        __syncthreads();
     }
 }
 
@@ -643,17 +691,14 @@ constexpr int kMaxCtas = 2 * 160;       // sizes the workspace: two CTAs per SM
 template <int D, int BITS, int NT>
 cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
 {
-    using C = RowsCfg<D, BITS, NT>;
-    auto kernel = attn_rows_kernel<D, BITS, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const int ctas = min(sm_count() * (NT == 1 ? 2 : 1), NT == 1 ? kMaxCtas : kMaxCtas / 2);
+    attn_rows_kernel<D, BITS, NT><<<ctas, kThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int ctas = min(sm_count() * (NT == 1 ? 2 : 1), kMaxCtas);
-    kernel<<<ctas, kThreads, C::kSmem, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    // the join's CTAs come up while the first kernel runs and wait for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, 4);
-    cfg.blockDim = dim3(D);
+    cfg.gridDim = dim3(ctas * kWarps);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -667,7 +712,8 @@ cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
 
 size_t rows_workspace(int d)
 {
-    return (size_t)kMaxCtas * (sizeof(int4) + 2 * 16 * (d + 2) * sizeof(float));
+    // 8 rows for each warp of two CTAs per SM, or 16 for each of one
+    return (size_t)kMaxCtas * kWarps * (sizeof(int4) + 2 * 8 * (d + 4) * sizeof(float));
 }
 
 cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
@@ -675,8 +721,8 @@ cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int
                               void *workspace, cudaStream_t stream)
 {
     int4 *joined = reinterpret_cast<int4 *>(workspace);
-    RowsArgs p{q, ldq, ldo, out, c, a, T, Hq, Hkv, Hq / Hkv, few, scale * 1.4426950408889634f,
-               reinterpret_cast<float *>(joined + kMaxCtas), joined};
+    RowsArgs p{q, ldq, ldo, out, c, a, T, Hq, Hkv, Hq / Hkv, few, scale * 1.4426950408889634f, 0x64006400u, 0x54005400u,
+               reinterpret_cast<float *>(joined + kMaxCtas * kWarps), joined};
     if (d == 128) {
         if (c.bits == 4) return eight ? launch_rows<128, 4, 1>(p, stream) : launch_rows<128, 4, 2>(p, stream);
         return eight ? launch_rows<128, 8, 1>(p, stream) : launch_rows<128, 8, 2>(p, stream);

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(
             const __half sh = __float2half_rz(__fdiv_rn(hi - lo, (float)((1 << BITS) - 1)));
             const float s = __half2float(sh);
             const int hk = is_k ? h - Hq : h - Hq - Hkv;
-            const size_t row = ((size_t)page * Hkv + hk) * a.page_size + s_pos[i] % a.page_size;
+            const size_t row = ((size_t)page * Hkv + hk) * a.page_size + (s_pos[i] & (a.page_size - 1));
             uint8_t *dst = (is_k ? c.k_codes : c.v_codes) + row * (D * BITS / 8);
             const uint64_t cx = codes8<BITS>(x, lo, s), cy = codes8<BITS>(y, lo, s);
             if (BITS == 4) {
