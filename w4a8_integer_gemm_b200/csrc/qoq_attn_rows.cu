@@ -10,16 +10,16 @@
 // the products run on the raw codes, exact in FP16, and the scales touch one
 // number per token.
 //
-// A warp works alone on its own tokens, without barriers or shared memory:
-// the cache's bytes go from global memory straight into the fragments of
+// A warp works alone on its own tokens, without block barriers, in
 // warp-level MMAs (m16n8k16, FP32 sums; the rows as the 8-wide N dimension):
 //     S^T[token][row]   = codes of K (A, tokens x channels) x q (B)
 //     O^T[channel][row] = codes of V^T (A, channels x tokens) x p s (B)
 // Which channel sits at which fragment position does not matter as long as
-// q, and O's write-out, agree; so a lane reads 16 neighbouring bytes of a key
-// and D/64 * BITS/2 of a value.  The weights go from the layout of S^T to that of B
-// by one 8x8 transposition (movmatrix) each.  The next group's loads are issued as
-// soon as the registers they fill have been consumed.
+// q, and O's write-out, agree; so a lane reads neighbouring bytes of a key or
+// a value.  The weights go from the layout of S^T to that of B by one 8x8
+// transposition (movmatrix) each.  A ring of three stages of 32 tokens (16 for
+// 8-bit heads of 128) per warp is filled by bulk copies, one per granule of 16
+// tokens and array, each issued by the lane that looked the page up.
 //
 // Running maximum m, sum l and sum of p m' in FP32; m may lag behind by 2^8,
 // so O is rescaled rarely.  The weights p s are rounded to FP16 (half a step
@@ -54,7 +54,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSwitch = 2;              // granules that a run counts for its beginning and end
 constexpr int kLeast = 4;               // granules of a warp's share, at least (a partial result costs about as much)
-constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint64_t kBudgetNs = 2000000000ull;
+
+__device__ int g_rows_error;            // non-zero after a bounded wait ran out
 
 struct RowsArgs {
     const uint16_t *q;
@@ -120,16 +122,16 @@ __device__ __forceinline__ uint32_t bytes_hi(uint32_t x, uint32_t e6)
 }
 
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w)
+__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t *w)
 {
     if (N == 1) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
     } else if (N == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
         w[0] = x.x;
         w[1] = x.y;
     } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
         w[0] = x.x;
         w[1] = x.y;
         w[2] = x.z;
@@ -143,8 +145,12 @@ struct RowsCfg {
     static constexpr int kKW = kRowBytes / 16;            // words of a key per lane
     static constexpr int kVW = kRowBytes / 32;            // words of a value per lane
     static constexpr int kMt = D / 16;                    // 16-channel tiles of O^T
-    static constexpr int kGr = D == 128 ? 1 : 2;   // 16-token granules per group (registers bound it)
+    static constexpr int kGr = BITS == 8 && D == 128 ? 1 : 2;   // 16-token granules per stage
     static constexpr int kGroup = 16 * kGr;               // tokens
+    static constexpr int kGranule = 16 * (2 * kRowBytes + 8);   // bytes: keys, values, their parameters
+    static constexpr int kStage = kGr * kGranule;
+    static constexpr int kStages = 3;
+    static constexpr int kSmem = kWarps * kStages * kStage;     // 102 KB (d = 128): two CTAs per SM
     static constexpr int kRows = 8 * NT;
     static constexpr int kStride = D + 4;                 // floats of a partial row
     static constexpr float kOff = BITS == 4 ? 8.0f : 128.0f;
@@ -158,6 +164,9 @@ template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(const RowsArgs p)
 {
     using C = RowsCfg<D, BITS, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];    // [kWarps][kStages][kStage]
+    __shared__ uint64_t s_bar[kWarps][C::kStages];
+    __shared__ int abort_flag;
     __shared__ long long s_sum[kWarps], s_before[kThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -198,7 +207,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             total += s_sum[w];
         }
         s_before[threadIdx.x] = x;
-        if (lane == 0) p.joined[me] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) {
+            p.joined[me] = make_int4(-1, 0, 0, 0);
+            for (int i = 0; i < C::kStages; ++i) mbar_init(smem_addr(&s_bar[warp][i]), 1);
+            fence_mbar_init();
+        }
+        if (threadIdx.x == 0) abort_flag = 0;
         __syncthreads();
         grid_launch_dependents();
         ctas = min((long long)gridDim.x * kWarps, (total + kLeast - 1) / kLeast);
@@ -224,6 +238,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         at -= skip % unit;                           // where the run begins; the share begins within it
     }
     long long from = total * me / ctas;              // where the warp's part of the run begins
+    uint8_t *ring_ptr = smem + warp * C::kStages * C::kStage;
+    const uint32_t ring = smem_addr(ring_ptr), bar = smem_addr(&s_bar[warp][0]);
+    uint32_t staged = 0, used = 0;                   // stages issued and consumed by the warp so far
+    uint32_t there = 0;                              // four bits per slot: which of its granules have a page
+    bool failed = false;
+    // byte selectors of the value pass
+    const uint32_t pick[2] = {BITS == 4 ? (c & 1 ? 0x1054u : 0x5410u) : (c & 1 ? 0x1504u : 0x5140u),
+                              BITS == 4 ? (c & 1 ? 0x3276u : 0x7632u) : (c & 1 ? 0x3726u : 0x7362u)};
 
     while (at < end) {
         const int b = run.b, hk = run.hk, rows = run.n * p.G - run.row0;
@@ -300,53 +322,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[t][mt][r] = 0.0f;
 
-        // ---- the tokens, kGr granules of 16 at a time ----
-        uint32_t kw[C::kGr][2][C::kKW], vw[C::kGr][4][C::kVW], kp[C::kGr][2], vp[C::kGr][2];
-        uint32_t base[C::kGr], base1[C::kGr];            // cache row of a granule's first token, or kNone: this group's, the next's
-        auto locate = [&](int tok, uint32_t (&bs)[C::kGr]) {
-#pragma unroll
-            for (int i = 0; i < C::kGr; ++i) {
-                const int pos = tok + 16 * i;
-                const int page = pos < tok1 ? page_of(a, b, pos) : -1;
-                bs[i] = page < 0 ? kNone : ((uint32_t)page * p.Hkv + hk) * a.page_size + (pos & (a.page_size - 1));
+        // ---- the tokens, a stage of kGr granules of 16 at a time, kStages of them in flight ----
+        // Copies of the n stages from `stage` on; lane (stage, granule, array) looks its page up and issues one.
+        auto issue = [&](int stage, int n) {
+            const int so = lane / (4 * C::kGr), gi = lane / 4 % C::kGr, kind = lane & 3;
+            const int pos = tok0 + (stage + so) * C::kGroup + 16 * gi;
+            const int page = so < n && pos < tok1 ? page_of(a, b, pos) : -1;
+            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+            const int slot = (int)((staged + so) % C::kStages);
+            if (so < n && lane % (4 * C::kGr) == 0) {
+                const uint32_t mine = have >> lane & (C::kGr == 1 ? 0x1u : 0x11u);
+                if (mine) mbar_arrive_expect_tx(bar + 8 * slot, __popc(mine) * C::kGranule);
+                else mbar_arrive(bar + 8 * slot);
             }
+            __syncwarp();
+            if (page >= 0) {
+                const size_t row = ((size_t)page * p.Hkv + hk) * a.page_size + (pos & (a.page_size - 1));
+                const bool val = kind & 1;
+                const uint8_t *src = kind < 2 ? (val ? p.c.v_codes : p.c.k_codes) + row * C::kRowBytes
+                                              : reinterpret_cast<const uint8_t *>(val ? p.c.v_par : p.c.k_par) + row * 4;
+                const uint32_t dst = ring + slot * C::kStage +
+                                     (kind < 2 ? (val * C::kGr + gi) * 16 * C::kRowBytes
+                                               : 2 * C::kGr * 16 * C::kRowBytes + (val * C::kGr + gi) * 64);
+                bulk_load(dst, src, kind < 2 ? 16 * C::kRowBytes : 64, bar + 8 * slot);
+            }
+#pragma unroll
+            for (int i = 0; i < C::kStages; ++i)
+                if (i < n) {
+                    const int s = (int)((staged + i) % C::kStages);
+                    there = (there & ~(0xFu << 4 * s)) | ((have >> 4 * C::kGr * i & 1u) | (have >> 4 * C::kGr * i >> 3 & 2u)) << 4 * s;
+                }
+            staged += n;
         };
-        // a lane's place in a granule: keys g and g + 8, values 2c, 2c + 1, 2c + 8, 2c + 9
-        const uint8_t *kc0 = p.c.k_codes + g * C::kRowBytes + (C::kKW >= 4 ? 16 : 4 * C::kKW) * c;
-        const uint8_t *vc0 = p.c.v_codes + 2 * c * C::kRowBytes + 4 * C::kVW * g;
-        const uint32_t *kp0 = reinterpret_cast<const uint32_t *>(p.c.k_par) + g;
-        const uint32_t *vp0 = reinterpret_cast<const uint32_t *>(p.c.v_par) + g;
-        auto load_k = [&](const uint32_t (&bs)[C::kGr]) {
+        const int stages = (tok1 - tok0 + C::kGroup - 1) / C::kGroup;     // 0 for an empty context
+        // (the last run's slots were read by ordinary loads and are refilled by asynchronous copies)
+        fence_proxy_async_smem();
+        __syncwarp();
+        issue(0, min(stages, C::kStages));
+        for (int stage = 0; stage < stages; ++stage, ++used) {
+            const int tok = tok0 + stage * C::kGroup, slot = (int)(used % C::kStages);
+            if (!__all_sync(0xffffffffu, wait_bounded(bar + 8 * slot, (uint32_t)(used / C::kStages) & 1, &abort_flag, kBudgetNs))) {
+                failed = true;
+                break;
+            }
+            const uint8_t *sk = ring_ptr + slot * C::kStage + g * C::kRowBytes + (C::kKW >= 4 ? 16 : 4 * C::kKW) * c;
+            // (lanes of odd c read the second token of a pair first: fewer bank conflicts)
+            const uint8_t *sv = ring_ptr + slot * C::kStage + (C::kGr * 16 + 2 * c + (c & 1)) * C::kRowBytes + 4 * C::kVW * g;
+            const int flip = c & 1 ? -C::kRowBytes : C::kRowBytes;
+            const uint32_t *sp = reinterpret_cast<const uint32_t *>(ring_ptr + slot * C::kStage + 2 * C::kGr * 16 * C::kRowBytes) + g;
+            uint32_t kp[C::kGr][2], vp[C::kGr][2];
+            bool gone[C::kGr];                               // the granule's page is absent
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
-                if (bs[i] == kNone) continue;
-                const uint8_t *src = kc0 + (size_t)bs[i] * C::kRowBytes;
-                const uint32_t *par = kp0 + bs[i];
+                gone[i] = !(there >> (4 * slot + i) & 1u);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    load_words<C::kKW < 4 ? C::kKW : 4>(src + 8 * h * C::kRowBytes, kw[i][h]);
-                    if (C::kKW == 8) load_words<4>(src + 8 * h * C::kRowBytes + 64, kw[i][h] + (C::kKW == 8 ? 4 : 0));
-                    kp[i][h] = __ldg(par + 8 * h);
+                    kp[i][h] = sp[16 * i + 8 * h];
+                    vp[i][h] = sp[16 * (C::kGr + i) + 8 * h];
                 }
             }
-        };
-        auto load_v = [&](const uint32_t (&bs)[C::kGr]) {
-#pragma unroll
-            for (int i = 0; i < C::kGr; ++i) {
-                if (bs[i] == kNone) continue;
-                const uint8_t *src = vc0 + (size_t)bs[i] * C::kRowBytes;
-                const uint32_t *par = vp0 + bs[i];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) load_words<C::kVW>(src + ((u & 1) + 8 * (u >> 1)) * C::kRowBytes, vw[i][u]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) vp[i][h] = __ldg(par + 8 * h);
-            }
-        };
-        locate(tok0, base);
-        load_k(base);
-        load_v(base);
-        locate(tok0 + 16 * C::kGr, base1);
-        for (int tok = tok0; tok < tok1; tok += 16 * C::kGr) {
             // scores, in log2 units
             float sc[C::kGr][NT][4];
 #pragma unroll
@@ -355,18 +389,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) sc[i][t][r] = 0.0f;
-                if (base[i] == kNone) continue;
+                if (gone[i]) continue;
+                uint32_t kw[2][C::kKW];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *src = sk + (16 * i + 8 * h) * C::kRowBytes;
+                    lds_words<C::kKW < 4 ? C::kKW : 4>(src, kw[h]);
+                    if (C::kKW == 8) lds_words<4>(src + 64, kw[h] + (C::kKW == 8 ? 4 : 0));
+                }
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t a0, a1, a2, a3;
                     if (BITS == 4) {
-                        const uint32_t x = kw[i][0][j / 2] >> (8 * (j & 1)), y = kw[i][1][j / 2] >> (8 * (j & 1));
+                        const uint32_t x = kw[0][j / 2] >> (8 * (j & 1)), y = kw[1][j / 2] >> (8 * (j & 1));
                         a0 = pair_lo(x, e6);
                         a1 = pair_lo(y, e6);
                         a2 = pair_hi(x, e5);
                         a3 = pair_hi(y, e5);
                     } else {
-                        const uint32_t x = kw[i][0][j % C::kKW], y = kw[i][1][j % C::kKW];
+                        const uint32_t x = kw[0][j % C::kKW], y = kw[1][j % C::kKW];
                         a0 = bytes_lo(x, e6);
                         a1 = bytes_lo(y, e6);
                         a2 = bytes_hi(x, e6);
@@ -377,13 +418,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 }
             }
             // Tokens that no row sees may hold anything: their parameters become zeros, so that nothing below is NaN.
-            const bool edge = tok + C::kGroup > see_min || base[0] == kNone || base[C::kGr - 1] == kNone;
+            const bool edge = tok + C::kGroup > see_min || gone[0] || gone[C::kGr - 1];
             if (edge) {
 #pragma unroll
                 for (int i = 0; i < C::kGr; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        if (base[i] == kNone || tok + 16 * i + g + 8 * h >= see_max) kp[i][h] = vp[i][h] = 0u;
+                        if (gone[i] || tok + 16 * i + g + 8 * h >= see_max) kp[i][h] = vp[i][h] = 0u;
             }
             float top[NT][2];
 #pragma unroll
@@ -409,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (base[i] == kNone || tok + 16 * i + g + 8 * (r >> 1) >= see[t][r & 1]) sc[i][t][r] = -INFINITY;
+                            if (gone[i] || tok + 16 * i + g + 8 * (r >> 1) >= see[t][r & 1]) sc[i][t][r] = -INFINITY;
             }
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i)
@@ -417,8 +458,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) top[t][r & 1] = fmaxf(top[t][r & 1], sc[i][t][r]);
-            // the key registers are free: the next group's
-            load_k(base1);
             bool grow = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -492,8 +531,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             }
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
-                if (base[i] == kNone) continue;
-                uint32_t pb[NT][2];
+                if (gone[i]) continue;
+                uint32_t pb[NT][2], vw[4][C::kVW];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) lds_words<C::kVW>(sv + (16 * i + 8 * (u >> 1)) * C::kRowBytes + (u & 1 ? flip : 0), vw[u]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -507,30 +548,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 };
 #pragma unroll
                 for (int w = 0; w < C::kVW; ++w) {
-                    if (BITS == 4) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // bytes 2h, 2h + 1 of one token under those of the next
-                            const uint32_t x = __byte_perm(vw[i][0][w], vw[i][1][w], h ? 0x7632 : 0x5410);
-                            const uint32_t y = __byte_perm(vw[i][2][w], vw[i][3][w], h ? 0x7632 : 0x5410);
+                    for (int h = 0; h < 2; ++h) {
+                        // 4 bits: bytes 2h, 2h + 1 of a token under those of the next; 8 bits: the two tokens' bytes in turn
+                        const uint32_t x = __byte_perm(vw[0][w], vw[1][w], pick[h]), y = __byte_perm(vw[2][w], vw[3][w], pick[h]);
+                        if (BITS == 4) {
                             tile(4 * w + 2 * h, pair_lo(x, e6), pair_hi(x, e5), pair_lo(y, e6), pair_hi(y, e5));
                             tile(4 * w + 2 * h + 1, pair_lo(x >> 8, e6), pair_hi(x >> 8, e5), pair_lo(y >> 8, e6), pair_hi(y >> 8, e5));
-                        }
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t x = __byte_perm(vw[i][0][w], vw[i][1][w], h ? 0x7362 : 0x5140);
-                            const uint32_t y = __byte_perm(vw[i][2][w], vw[i][3][w], h ? 0x7362 : 0x5140);
+                        } else {
                             tile(2 * w + h, bytes_lo(x, e6), bytes_hi(x, e6), bytes_lo(y, e6), bytes_hi(y, e6));
                         }
                     }
                 }
             }
-            load_v(base1);
-#pragma unroll
-            for (int i = 0; i < C::kGr; ++i) base[i] = base1[i];
-            locate(tok + 32 * C::kGr, base1);
+            if (stage + C::kStages < stages) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                issue(stage + C::kStages, 1);
+            }
         }
+        if (failed) break;
 
         // ---- finish, or leave a partial result ----
         const bool begins = g0 == 0, ends = g1 == run.grains;
@@ -600,74 +637,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             }
         }
     }
+    if (failed) {
+        // a wait ran out: report it, and let the copies in flight land before the shared memory goes away
+        if (lane == 0) atomicExch(&g_rows_error, 1);
+        const uint64_t stop = global_timer_ns() + 200000000ull;
+        for (; used < staged; ++used)
+            while (!mbar_try_wait(bar + 8 * (used % C::kStages), (used / C::kStages) & 1) && global_timer_ns() < stop) {
+            }
+    }
 }
 
-// One CTA per warp of the first kernel: joins the run that ended in its
-// share.  Its warps take every eighth part, a lane four channels of all rows;
-// the warps' sums are joined in order.
+// Joins the runs that span warps.  CTA (x, y) looks at eight warps' ends and
+// takes rows 2y and 2y + 1 of each run that ended there; eight of its 16
+// warps share a row's parts, four in flight at a time, and the sums are
+// joined in order.  A lane holds D / 32 channels.
+constexpr int kJoinThreads = 512;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs p)
+__global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const RowsArgs p)
 {
-    constexpr int kRows = 8 * NT, kStride = D + 4;
-    __shared__ float4 s_v[kWarps][8][D / 4];
-    __shared__ float2 s_ml[kWarps][8];
-    grid_dependency_wait();
-    const int4 j = p.joined[blockIdx.x];
-    if (j.x < 0) return;
+    constexpr int kRows = 8 * NT, kStride = D + 4, kN = D / 32;
+    __shared__ float s_v[2][8][D];
+    __shared__ float2 s_ml[2][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t_seq = __ldg(p.a.cu + j.x), n = __ldg(p.a.cu + j.x + 1) - t_seq, rows = min(kRows, n * p.G - j.y);
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        float4 v[8];
-        float M[8], L[8];
+    const int half = warp >> 3, w8 = warp & 7;
+    grid_dependency_wait();
+    for (int e = 0; e < 8; ++e) {
+        const int last = blockIdx.x * 8 + e;
+        const int4 j = p.joined[last];
+        if (j.x < 0) continue;
+        const int t_seq = __ldg(p.a.cu + j.x), n = __ldg(p.a.cu + j.x + 1) - t_seq, rows = min(kRows, n * p.G - j.y);
+        const int row = 2 * blockIdx.y + half;
+        if (2 * (int)blockIdx.y >= rows) continue;           // the same for the whole CTA
+        float v[kN], M = -INFINITY, L = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            M[i] = -INFINITY;
-            L[i] = 0.0f;
-        }
-        for (int w = j.w + warp; w <= (int)blockIdx.x; w += kWarps) {
-            const float *part = p.part + ((size_t)w * 2 + (w == j.w ? 1 : 0)) * kRows * kStride;
+        for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+        if (row < rows) {
+            for (int w = j.w + w8; w <= last; w += 32) {
+                float y[4][kN];
+                float2 ml[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (r0 + i >= rows) break;
-                const float *x = part + (r0 + i) * kStride;
-                const float2 ml = *reinterpret_cast<const float2 *>(x + D);
-                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (lane < D / 4) y = *reinterpret_cast<const float4 *>(x + 4 * lane);
-                const float m1 = fmaxf(M[i], ml.x);
-                const float f0 = M[i] == -INFINITY ? 0.0f : exp2_fast(M[i] - m1), f1 = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m1);
-                M[i] = m1;
-                L[i] = fmaf(L[i], f0, ml.y * f1);
-                v[i] = make_float4(fmaf(v[i].x, f0, y.x * f1), fmaf(v[i].y, f0, y.y * f1), fmaf(v[i].z, f0, y.z * f1),
-                                   fmaf(v[i].w, f0, y.w * f1));
+                for (int u = 0; u < 4; ++u) {
+                    ml[u] = make_float2(-INFINITY, 0.0f);
+                    if (w + 8 * u > last) continue;
+                    const float *x = p.part + (((size_t)(w + 8 * u) * 2 + (w + 8 * u == j.w ? 1 : 0)) * kRows + row) * kStride;
+                    ml[u] = *reinterpret_cast<const float2 *>(x + D);
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) y[u][i] = x[32 * i + lane];
+                }
+                const float m1 = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+                if (m1 == -INFINITY) continue;
+                const float f0 = M == -INFINITY ? 0.0f : exp2_fast(M - m1);
+                M = m1;
+                L *= f0;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) v[i] *= f0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (ml[u].x == -INFINITY) continue;
+                    const float f = exp2_fast(ml[u].x - m1);
+                    L = fmaf(ml[u].y, f, L);
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) v[i] = fmaf(y[u][i], f, v[i]);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (lane < D / 4) s_v[warp][i][lane] = v[i];
-            if (lane == 0) s_ml[warp][i] = make_float2(M[i], L[i]);
-        }
+        for (int i = 0; i < kN; ++i) s_v[half][w8][32 * i + lane] = v[i];
+        if (lane == 0) s_ml[half][w8] = make_float2(M, L);
         __syncthreads();
-        // warp i finishes row i
-        if (r0 + warp < rows && lane < D / 4) {
-            float m = -INFINITY, l = 0.0f;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int x = threadIdx.x; x < 2 * D; x += kJoinThreads) {
+            const int hf = x / D, ch = x % D, r = j.y + 2 * blockIdx.y + hf;
+            if (2 * (int)blockIdx.y + hf >= rows) continue;
+            float m = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][warp].x);
+            for (int w = 0; w < 8; ++w) m = fmaxf(m, s_ml[hf][w].x);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = s_ml[w][warp];
-                const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m);
-                const float4 y = s_v[w][warp][lane];
-                l = fmaf(ml.y, f, l);
-                x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+            for (int w = 0; w < 8; ++w) {
+                const float f = s_ml[hf][w].x == -INFINITY ? 0.0f : exp2_fast(s_ml[hf][w].x - m);
+                l = fmaf(s_ml[hf][w].y, f, l);
+                o = fmaf(s_v[hf][w][ch], f, o);
             }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const int r = j.y + r0 + warp;
-            const __half2 h0 = __floats2half2_rn(x.x * inv, x.y * inv), h1 = __floats2half2_rn(x.z * inv, x.w * inv);
-            *reinterpret_cast<uint2 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + 4 * lane) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+            p.out[(int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + ch] =
+                float_to_half_bits(l > 0.0f ? o / l : 0.0f);
         }
         __syncthreads();
     }
@@ -692,13 +744,17 @@ template <int D, int BITS, int NT>
 cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
 {
     const int ctas = min(sm_count() * (NT == 1 ? 2 : 1), NT == 1 ? kMaxCtas : kMaxCtas / 2);
-    attn_rows_kernel<D, BITS, NT><<<ctas, kThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    constexpr int smem = RowsCfg<D, BITS, NT>::kSmem;
+    auto kernel = attn_rows_kernel<D, BITS, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<ctas, kThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // the join's CTAs come up while the first kernel runs and wait for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas * kWarps);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(ctas * kWarps / 8, 4 * NT);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -729,6 +785,20 @@ cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int
     }
     if (c.bits == 4) return eight ? launch_rows<64, 4, 1>(p, stream) : launch_rows<64, 4, 2>(p, stream);
     return eight ? launch_rows<64, 8, 1>(p, stream) : launch_rows<64, 8, 2>(p, stream);
+}
+
+cudaError_t read_and_clear_rows_error(int *value)
+{
+    *value = 0;
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_rows_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_rows_error, &zero, sizeof(int));
+    }
+    *value = v;
+    return e;
 }
 
 }  // namespace qoq
