@@ -398,12 +398,11 @@ int qoq_set_linear_in_kernel_quant(int enable)
 
 int qoq_device_error(void *stream)
 {
-    int v = 0, w = 0, x = 0, y = 0;
+    int v = 0, w = 0, x = 0;
     if (qoq::read_and_clear_device_error((cudaStream_t)stream, &v) != cudaSuccess) return QOQ_ERR_CUDA;
     if (qoq::read_and_clear_kv4_error(&w) != cudaSuccess) return QOQ_ERR_CUDA;
     if (qoq::read_and_clear_tile_error(&x) != cudaSuccess) return QOQ_ERR_CUDA;
-    if (qoq::read_and_clear_rows_error(&y) != cudaSuccess) return QOQ_ERR_CUDA;
-    return (v || w || x || y) ? QOQ_ERR_TIMEOUT : QOQ_OK;
+    return (v || w || x) ? QOQ_ERR_TIMEOUT : QOQ_OK;
 }
 
 }  // extern "C"

@@ -76,9 +76,8 @@ size_t rows_workspace(int d);
 cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                               const AttnBatch &a, int few, bool eight, float scale, uint16_t *out, int64_t ldo,
                               void *workspace, cudaStream_t stream);
-// The kernels' error flags (a bounded wait ran out), read and cleared.
+// The tile kernel's error flag (a bounded wait ran out), read and cleared.
 cudaError_t read_and_clear_tile_error(int *value);
-cudaError_t read_and_clear_rows_error(int *value);
 cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream);

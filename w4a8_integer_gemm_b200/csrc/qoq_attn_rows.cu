@@ -3,23 +3,26 @@
 //
 // Bound: the cache's bytes, read once.  What has to stay below that is the
 // instructions that turn codes into tensor-core operands, so a code is never
-// scaled on its own: with x = s c + m per token (c centred: c' = c - off,
-// m' = m + off s)
-//     score_j = s_j (q . c'_j) + m'_j sum(q)
-//     out     = sum_j (p_j s_j) c'_j + sum_j p_j m'_j
-// the products run on the raw codes, exact in FP16, and the scales touch one
-// number per token.
+// scaled on its own: with x = s c + m per token,
+//     score_j = s_j (q . c_j) + m_j sum(q)
+//     out     = sum_j (p_j s_j) c'_j + sum_j p_j m'_j    (c' = c - off, m' = m + off s)
+// the products run on the codes, and the scales touch one number per token.
+// Values are centred (off: 8 or 128), because their sum's terms should cancel
+// in the tensor core and not against sum p m'.
 //
 // A warp works alone on its own tokens, without block barriers, in
-// warp-level MMAs (m16n8k16, FP32 sums; the rows as the 8-wide N dimension):
-//     S^T[token][row]   = codes of K (A, tokens x channels) x q (B)
-//     O^T[channel][row] = codes of V^T (A, channels x tokens) x p s (B)
+// warp-level MMAs with the rows as the 8-wide N dimension:
+//     S^T[token][row]   = codes of K (A, tokens x channels) x q (B), m16n8k32 on
+//                         integers, exact: the codes are 8-bit operands after one
+//                         mask each (none for 8 bits; FP16 operands took four times
+//                         the instructions), and q is two 8-bit digits, 2^-15 of the
+//                         row's largest |q|
+//     O^T[channel][row] = codes of V^T (A, channels x tokens) x p s (B), m16n8k16, FP16
 // Which channel sits at which fragment position does not matter as long as
 // q, and O's write-out, agree; so a lane reads neighbouring bytes of a key or
 // a value.  The weights go from the layout of S^T to that of B by one 8x8
-// transposition (movmatrix) each.  A ring of three stages of 32 tokens (16 for
-// 8-bit heads of 128) per warp is filled by bulk copies, one per granule of 16
-// tokens and array, each issued by the lane that looked the page up.
+// transposition (movmatrix) each.  Each warp has a ring of three stages of 32
+// tokens (16 for 8-bit heads of 128), filled by asynchronous copies.
 //
 // Running maximum m, sum l and sum of p m' in FP32; m may lag behind by 2^8,
 // so O is rescaled rarely.  The weights p s are rounded to FP16 (half a step
@@ -54,9 +57,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSwitch = 2;              // granules that a run counts for its beginning and end
 constexpr int kLeast = 4;               // granules of a warp's share, at least (a partial result costs about as much)
-constexpr uint64_t kBudgetNs = 2000000000ull;
-
-__device__ int g_rows_error;            // non-zero after a bounded wait ran out
 
 struct RowsArgs {
     const uint16_t *q;
@@ -81,6 +81,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D (16 x 8, INT32) += A (16 x 32, UINT8, row) * B (32 x 8, INT8, col).
+__device__ __forceinline__ void mma16832(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
@@ -147,8 +156,7 @@ struct RowsCfg {
     static constexpr int kMt = D / 16;                    // 16-channel tiles of O^T
     static constexpr int kGr = BITS == 8 && D == 128 ? 1 : 2;   // 16-token granules per stage
     static constexpr int kGroup = 16 * kGr;               // tokens
-    static constexpr int kGranule = 16 * (2 * kRowBytes + 8);   // bytes: keys, values, their parameters
-    static constexpr int kStage = kGr * kGranule;
+    static constexpr int kStage = kGr * (32 * kRowBytes + 128); // bytes: keys, values, their parameters
     static constexpr int kStages = 3;
     static constexpr int kSmem = kWarps * kStages * kStage;     // 102 KB (d = 128): two CTAs per SM
     static constexpr int kRows = 8 * NT;
@@ -165,8 +173,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 {
     using C = RowsCfg<D, BITS, NT>;
     extern __shared__ __align__(128) uint8_t smem[];    // [kWarps][kStages][kStage]
-    __shared__ uint64_t s_bar[kWarps][C::kStages];
-    __shared__ int abort_flag;
     __shared__ long long s_sum[kWarps], s_before[kThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -207,12 +213,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             total += s_sum[w];
         }
         s_before[threadIdx.x] = x;
-        if (lane == 0) {
-            p.joined[me] = make_int4(-1, 0, 0, 0);
-            for (int i = 0; i < C::kStages; ++i) mbar_init(smem_addr(&s_bar[warp][i]), 1);
-            fence_mbar_init();
-        }
-        if (threadIdx.x == 0) abort_flag = 0;
+        if (lane == 0) p.joined[me] = make_int4(-1, 0, 0, 0);
         __syncthreads();
         grid_launch_dependents();
         ctas = min((long long)gridDim.x * kWarps, (total + kLeast - 1) / kLeast);
@@ -239,10 +240,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
     }
     long long from = total * me / ctas;              // where the warp's part of the run begins
     uint8_t *ring_ptr = smem + warp * C::kStages * C::kStage;
-    const uint32_t ring = smem_addr(ring_ptr), bar = smem_addr(&s_bar[warp][0]);
-    uint32_t staged = 0, used = 0;                   // stages issued and consumed by the warp so far
-    uint32_t there = 0;                              // four bits per slot: which of its granules have a page
-    bool failed = false;
+    const uint32_t ring = smem_addr(ring_ptr);
+    // the lane's parameter of a granule: token lane % 16, of the key or the value
+    const int my_par = 2 * C::kGr * 16 * C::kRowBytes + (lane & 7) * 16 + ((lane >> 4) * 2 + (lane >> 3 & 1)) * 4;
     // byte selectors of the value pass
     const uint32_t pick[2] = {BITS == 4 ? (c & 1 ? 0x1054u : 0x5410u) : (c & 1 ? 0x1504u : 0x5140u),
                               BITS == 4 ? (c & 1 ? 0x3276u : 0x7632u) : (c & 1 ? 0x3726u : 0x7362u)};
@@ -256,61 +256,84 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         const int t_seq = __ldg(a.cu + b);
         const int tok0 = 16 * g0, tok1 = min(16 * g1, len);
 
-        // ---- q fragments, sums, limits of the lane's columns ----
-        uint32_t qf[NT][D / 16][2];
-        float sq[NT][2], m[NT][2], l[NT][2], W[NT][2];
+        // ---- q: two 8-bit digits per channel, sums, limits of the lane's columns ----
+        uint32_t qf[NT][2][D / 32][2];                   // [.][high, low digit][MMA step][fragment register]
+        float sq[NT][2], qs[NT][2];                      // sum of q, value of a unit of its digits; log2 units
+        float m[NT][2], l[NT][2], W[NT][2];
         float k = 0.0f;                                  // power of two on the value scales; 0: none seen yet
-        int see[NT][2], see_max = 0;
+        int see[NT][2], see_min = 1 << 30, see_max = 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int row = 8 * t + g;
-            const uint16_t *src = nullptr;
-            if (row < rows) {
-                const int r = run.row0 + row;
-                src = p.q + (int64_t)(t_seq + r / p.G) * p.ldq + (size_t)(hk * p.G + r % p.G) * D;
-            }
-            float s = 0.0f;
-            if (BITS == 4) {
-#pragma unroll
-                for (int j = 0; j < C::kKW; ++j) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (src) x = to_code_order(__ldg(reinterpret_cast<const uint4 *>(src + (D / 4) * c + 8 * j)));
-                    qf[t][2 * j][0] = x.x;
-                    qf[t][2 * j][1] = x.y;
-                    qf[t][2 * j + 1][0] = x.z;
-                    qf[t][2 * j + 1][1] = x.w;
+            // the lane's channels in the order its key words expand to: byte i of step j's registers 0 and 1 are
+            // 4 bits: (D/4) c + 8 j + 2 i and the next; 8 bits: byte i of words 2j and 2j + 1
+            __half x[D / 32][2][4];
+            {
+                const uint16_t *src = nullptr;
+                if (row < rows) {
+                    const int r = run.row0 + row;
+                    src = p.q + (int64_t)(t_seq + r / p.G) * p.ldq + (size_t)(hk * p.G + r % p.G) * D;
                 }
-            } else {
 #pragma unroll
-                for (int j = 0; j < C::kKW; ++j) {
-                    uint2 x = make_uint2(0, 0);
-                    if (src) x = __ldg(reinterpret_cast<const uint2 *>(src + 64 * (j / 4) + 16 * c + 4 * (j % 4)));
-                    qf[t][j][0] = x.x;
-                    qf[t][j][1] = x.y;
+                for (int j = 0; j < D / 32; ++j) {
+                    uint4 y = make_uint4(0, 0, 0, 0);
+                    if (src) {
+                        const int ch = BITS == 4 ? (D / 4) * c + 8 * j : 64 * (j / 2) + 16 * c + 8 * (j % 2);
+                        y = __ldg(reinterpret_cast<const uint4 *>(src + ch));
+                    }
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const __half h = __ushort_as_half((uint16_t)(w[e / 2] >> (16 * (e & 1))));
+                        if (BITS == 4) x[j][e & 1][e / 2] = h;
+                        else x[j][e / 4][e & 3] = h;
+                    }
                 }
             }
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
+            for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const __half2 h = *reinterpret_cast<const __half2 *>(&qf[t][j][u]);
-                    s += __half2float(h.x) + __half2float(h.y);
+                for (int e = 0; e < 8; ++e) {
+                    top = fmaxf(top, fabsf(__half2float(x[j][e / 4][e & 3])));
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float inv = top > 0.0f ? 16256.0f / top : 0.0f;
+            int s = 0;                                   // of the digits: q's rounding then meets s c + m, not s c alone
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int v = __float2int_rn(__half2float(x[j][h][i]) * inv);    // -16256 .. 16256
+                        s += v;
+                        const int d = (v + 64) >> 7;                                     // v = 128 d + (-64 .. 63)
+                        hi |= (uint32_t)(d & 0xFF) << (8 * i);
+                        lo |= (uint32_t)((v - 128 * d) & 0xFF) << (8 * i);
+                    }
+                    qf[t][0][j][h] = hi;
+                    qf[t][1][j][h] = lo;
                 }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int col = 8 * t + 2 * c + u;
-                sq[t][u] = __shfl_sync(0xffffffffu, s, (2 * c + u) * 4) * p.scale_log2;
-                see[t][u] = col < rows ? first + (run.row0 + col) / p.G + 1 : 0;
-                see_max = max(see_max, see[t][u]);
+                qs[t][u] = __shfl_sync(0xffffffffu, top, (2 * c + u) * 4) * (p.scale_log2 / 16256.0f);
+                sq[t][u] = (float)__shfl_sync(0xffffffffu, s, (2 * c + u) * 4) * qs[t][u];
+                const bool real = col < rows;            // others' results go nowhere
+                see[t][u] = real ? first + (run.row0 + col) / p.G + 1 : 1 << 30;
+                if (real) {
+                    see_min = min(see_min, see[t][u]);
+                    see_max = max(see_max, see[t][u]);
+                }
                 m[t][u] = -INFINITY;
                 l[t][u] = W[t][u] = 0.0f;
             }
         }
-        int see_min = see[0][0];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) see_min = min(see_min, min(see[t][0], see[t][1]));
         see_min = __reduce_min_sync(0xffffffffu, see_min);
         see_max = __reduce_max_sync(0xffffffffu, see_max);
 
@@ -323,73 +346,69 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int r = 0; r < 4; ++r) o[t][mt][r] = 0.0f;
 
         // ---- the tokens, a stage of kGr granules of 16 at a time, kStages of them in flight ----
-        // Copies of the n stages from `stage` on; lane (stage, granule, array) looks its page up and issues one.
-        auto issue = [&](int stage, int n) {
-            const int so = lane / (4 * C::kGr), gi = lane / 4 % C::kGr, kind = lane & 3;
-            const int pos = tok0 + (stage + so) * C::kGroup + 16 * gi;
-            const int page = so < n && pos < tok1 ? page_of(a, b, pos) : -1;
-            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-            const int slot = (int)((staged + so) % C::kStages);
-            if (so < n && lane % (4 * C::kGr) == 0) {
-                const uint32_t mine = have >> lane & (C::kGr == 1 ? 0x1u : 0x11u);
-                if (mine) mbar_arrive_expect_tx(bar + 8 * slot, __popc(mine) * C::kGranule);
-                else mbar_arrive(bar + 8 * slot);
-            }
-            __syncwarp();
-            if (page >= 0) {
-                const size_t row = ((size_t)page * p.Hkv + hk) * a.page_size + (pos & (a.page_size - 1));
-                const bool val = kind & 1;
-                const uint8_t *src = kind < 2 ? (val ? p.c.v_codes : p.c.k_codes) + row * C::kRowBytes
-                                              : reinterpret_cast<const uint8_t *>(val ? p.c.v_par : p.c.k_par) + row * 4;
-                const uint32_t dst = ring + slot * C::kStage +
-                                     (kind < 2 ? (val * C::kGr + gi) * 16 * C::kRowBytes
-                                               : 2 * C::kGr * 16 * C::kRowBytes + (val * C::kGr + gi) * 64);
-                bulk_load(dst, src, kind < 2 ? 16 * C::kRowBytes : 64, bar + 8 * slot);
-            }
+        // Copies of one stage into slot `to`: every lane brings 16 bytes of each 512 of a granule's keys and values
+        // and one parameter, to where the lane that needs a token's four finds them side by side.  Returns a bit per
+        // granule that has a page.  (Bulk copies issued by single lanes take uniform registers: 80 instructions per
+        // granule against 20.)
+        auto copy = [&](int tok, int to) -> uint32_t {
+            uint32_t have = 0;
 #pragma unroll
-            for (int i = 0; i < C::kStages; ++i)
-                if (i < n) {
-                    const int s = (int)((staged + i) % C::kStages);
-                    there = (there & ~(0xFu << 4 * s)) | ((have >> 4 * C::kGr * i & 1u) | (have >> 4 * C::kGr * i >> 3 & 2u)) << 4 * s;
+            for (int i = 0; i < C::kGr; ++i) {
+                const int pos = tok + 16 * i, page = pos < tok1 ? page_of(a, b, pos) : -1;
+                if (page >= 0) {
+                    have |= 1u << i;
+                    const uint32_t row = ((uint32_t)page * p.Hkv + hk) * a.page_size + (pos & (a.page_size - 1));
+                    const uint8_t *kc = p.c.k_codes + (size_t)row * C::kRowBytes + 16 * lane;
+                    const uint8_t *vc = p.c.v_codes + (size_t)row * C::kRowBytes + 16 * lane;
+                    const uint32_t dk = ring + to * C::kStage + i * 16 * C::kRowBytes + 16 * lane;
+                    const uint32_t dv = dk + C::kGr * 16 * C::kRowBytes;
+#pragma unroll
+                    for (int e = 0; e < 16 * C::kRowBytes; e += 512) {
+                        cp_async<16>(dk + e, kc + e);
+                        cp_async<16>(dv + e, vc + e);
+                    }
+                    cp_async<4>(ring + to * C::kStage + my_par + 128 * i,
+                                reinterpret_cast<const uint32_t *>(lane < 16 ? p.c.k_par : p.c.v_par) + row + (lane & 15));
                 }
-            staged += n;
+            }
+            cp_async_commit();
+            return have;
         };
         const int stages = (tok1 - tok0 + C::kGroup - 1) / C::kGroup;     // 0 for an empty context
-        // (the last run's slots were read by ordinary loads and are refilled by asynchronous copies)
-        fence_proxy_async_smem();
-        __syncwarp();
-        issue(0, min(stages, C::kStages));
-        for (int stage = 0; stage < stages; ++stage, ++used) {
-            const int tok = tok0 + stage * C::kGroup, slot = (int)(used % C::kStages);
-            if (!__all_sync(0xffffffffu, wait_bounded(bar + 8 * slot, (uint32_t)(used / C::kStages) & 1, &abort_flag, kBudgetNs))) {
-                failed = true;
-                break;
-            }
+        uint32_t there = 0;                              // four bits per stage, the next one lowest: its granules have a page
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) there |= copy(tok0 + i * C::kGroup, i) << (4 * i);
+        int slot = 0;
+        for (int stage = 0; stage < stages; ++stage) {
+            const int tok = tok0 + stage * C::kGroup;
+            // the slot that the last stage left is filled again
+            there |= copy(tok + (C::kStages - 1) * C::kGroup, slot == 0 ? C::kStages - 1 : slot - 1) << (4 * (C::kStages - 1));
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();
             const uint8_t *sk = ring_ptr + slot * C::kStage + g * C::kRowBytes + (C::kKW >= 4 ? 16 : 4 * C::kKW) * c;
             // (lanes of odd c read the second token of a pair first: fewer bank conflicts)
             const uint8_t *sv = ring_ptr + slot * C::kStage + (C::kGr * 16 + 2 * c + (c & 1)) * C::kRowBytes + 4 * C::kVW * g;
             const int flip = c & 1 ? -C::kRowBytes : C::kRowBytes;
-            const uint32_t *sp = reinterpret_cast<const uint32_t *>(ring_ptr + slot * C::kStage + 2 * C::kGr * 16 * C::kRowBytes) + g;
+            const uint4 *sp = reinterpret_cast<const uint4 *>(ring_ptr + slot * C::kStage + 2 * C::kGr * 16 * C::kRowBytes) + g;
             uint32_t kp[C::kGr][2], vp[C::kGr][2];
             bool gone[C::kGr];                               // the granule's page is absent
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
-                gone[i] = !(there >> (4 * slot + i) & 1u);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    kp[i][h] = sp[16 * i + 8 * h];
-                    vp[i][h] = sp[16 * (C::kGr + i) + 8 * h];
-                }
+                gone[i] = !(there >> i & 1u);
+                const uint4 x = sp[8 * i];
+                kp[i][0] = x.x;
+                kp[i][1] = x.y;
+                vp[i][0] = x.z;
+                vp[i][1] = x.w;
             }
-            // scores, in log2 units
-            float sc[C::kGr][NT][4];
+            // q . codes, exact in 32-bit integers
+            int acc[C::kGr][NT][2][4];
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sc[i][t][r] = 0.0f;
-                if (gone[i]) continue;
+                    for (int r = 0; r < 8; ++r) acc[i][t][r / 4][r % 4] = 0;
                 uint32_t kw[2][C::kKW];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -398,23 +417,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     if (C::kKW == 8) lds_words<4>(src + 64, kw[h] + (C::kKW == 8 ? 4 : 0));
                 }
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    uint32_t a0, a1, a2, a3;
+                for (int j = 0; j < D / 32; ++j) {
+                    uint32_t f[4];
                     if (BITS == 4) {
-                        const uint32_t x = kw[0][j / 2] >> (8 * (j & 1)), y = kw[1][j / 2] >> (8 * (j & 1));
-                        a0 = pair_lo(x, e6);
-                        a1 = pair_lo(y, e6);
-                        a2 = pair_hi(x, e5);
-                        a3 = pair_hi(y, e5);
+                        f[0] = kw[0][j % C::kKW] & 0x0F0F0F0Fu;
+                        f[1] = kw[1][j % C::kKW] & 0x0F0F0F0Fu;
+                        f[2] = kw[0][j % C::kKW] >> 4 & 0x0F0F0F0Fu;
+                        f[3] = kw[1][j % C::kKW] >> 4 & 0x0F0F0F0Fu;
                     } else {
-                        const uint32_t x = kw[0][j % C::kKW], y = kw[1][j % C::kKW];
-                        a0 = bytes_lo(x, e6);
-                        a1 = bytes_lo(y, e6);
-                        a2 = bytes_hi(x, e6);
-                        a3 = bytes_hi(y, e6);
+                        f[0] = kw[0][2 * j % C::kKW];
+                        f[1] = kw[1][2 * j % C::kKW];
+                        f[2] = kw[0][(2 * j + 1) % C::kKW];
+                        f[3] = kw[1][(2 * j + 1) % C::kKW];
                     }
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(sc[i][t], a0, a1, a2, a3, qf[t][j][0], qf[t][j][1]);
+                    for (int t = 0; t < NT; ++t) {
+                        mma16832(acc[i][t][0], f, qf[t][0][j][0], qf[t][0][j][1]);
+                        mma16832(acc[i][t][1], f, qf[t][1][j][0], qf[t][1][j][1]);
+                    }
                 }
             }
             // Tokens that no row sees may hold anything: their parameters become zeros, so that nothing below is NaN.
@@ -426,22 +446,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     for (int h = 0; h < 2; ++h)
                         if (gone[i] || tok + 16 * i + g + 8 * h >= see_max) kp[i][h] = vp[i][h] = 0u;
             }
-            float top[NT][2];
+            // scores in log2 units, above the maximum in use
+            float sc[C::kGr][NT][4], base[NT][2], top[NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    base[t][u] = m[t][u] == -INFINITY ? 0.0f : -m[t][u];
+                    top[t][u] = -INFINITY;
+                }
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
                 float ks[2], km[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float s = half_bits_to_float((uint16_t)(kp[i][h] & 0xFFFFu));
-                    km[h] = fmaf(C::kOff, s, half_bits_to_float((uint16_t)(kp[i][h] >> 16)));
-                    ks[h] = s * p.scale_log2;
+                    ks[h] = half_bits_to_float((uint16_t)(kp[i][h] & 0xFFFFu));
+                    km[h] = half_bits_to_float((uint16_t)(kp[i][h] >> 16));
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sc[i][t][r] = fmaf(sc[i][t][r], ks[r >> 1], km[r >> 1] * sq[t][r & 1]);
+                    for (int r = 0; r < 4; ++r)
+                        sc[i][t][r] = fmaf((float)(acc[i][t][0][r] * 128 + acc[i][t][1][r]), ks[r >> 1] * qs[t][r & 1],
+                                           fmaf(km[r >> 1], sq[t][r & 1], base[t][r & 1]));
             }
             if (edge) {
 #pragma unroll
@@ -462,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) grow |= top[t][u] > m[t][u] + 8.0f;
+                for (int u = 0; u < 2; ++u) grow |= m[t][u] == -INFINITY ? top[t][u] > -INFINITY : top[t][u] > 8.0f;
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -472,15 +499,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        const float m1 = fmaxf(m[t][u], x);
-                        const float keep = m[t][u] == -INFINITY ? 0.0f : exp2_fast(m[t][u] - m1);
-                        m[t][u] = m1;
+                        // by how much the maximum in use grows (from 0 while there is none)
+                        const float up = m[t][u] == -INFINITY ? (x == -INFINITY ? 0.0f : x) : fmaxf(x, 0.0f);
+                        const float keep = m[t][u] == -INFINITY ? 1.0f : exp2_fast(-up);
+                        if (x > -INFINITY) m[t][u] = (m[t][u] == -INFINITY ? 0.0f : m[t][u]) + up;
                         l[t][u] *= keep;
                         W[t][u] *= keep;
 #pragma unroll
                         for (int mt = 0; mt < C::kMt; ++mt) {
                             o[t][mt][u] *= keep;
                             o[t][mt][2 + u] *= keep;
+                        }
+#pragma unroll
+                        for (int i = 0; i < C::kGr; ++i) {
+                            sc[i][t][u] -= up;
+                            sc[i][t][2 + u] -= up;
                         }
                     }
             }
@@ -511,11 +544,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                         for (int r = 0; r < 4; ++r) o[t][mt][r] *= f;
             }
             // weights: sc becomes p s k
-            float sub[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) sub[t][u] = m[t][u] == -INFINITY ? 0.0f : m[t][u];
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
                 const float vk[2] = {vs[i][0] * k, vs[i][1] * k};
@@ -523,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float w = exp2_fast(sc[i][t][r] - sub[t][r & 1]);
+                        const float w = exp2_fast(sc[i][t][r]);
                         l[t][r & 1] += w;
                         W[t][r & 1] = fmaf(w, vm[i][r >> 1], W[t][r & 1]);
                         sc[i][t][r] = w * vk[r >> 1];
@@ -531,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             }
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
-                if (gone[i]) continue;
                 uint32_t pb[NT][2], vw[4][C::kVW];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) lds_words<C::kVW>(sv + (16 * i + 8 * (u >> 1)) * C::kRowBytes + (u & 1 ? flip : 0), vw[u]);
@@ -561,13 +588,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     }
                 }
             }
-            if (stage + C::kStages < stages) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(stage + C::kStages, 1);
-            }
+            there >>= 4;
+            slot = slot + 1 == C::kStages ? 0 : slot + 1;
+            __syncwarp();
         }
-        if (failed) break;
+        cp_async_wait<0>();
+        __syncwarp();
 
         // ---- finish, or leave a partial result ----
         const bool begins = g0 == 0, ends = g1 == run.grains;
@@ -636,14 +662,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 }
             }
         }
-    }
-    if (failed) {
-        // a wait ran out: report it, and let the copies in flight land before the shared memory goes away
-        if (lane == 0) atomicExch(&g_rows_error, 1);
-        const uint64_t stop = global_timer_ns() + 200000000ull;
-        for (; used < staged; ++used)
-            while (!mbar_try_wait(bar + 8 * (used % C::kStages), (used / C::kStages) & 1) && global_timer_ns() < stop) {
-            }
     }
 }
 
@@ -785,20 +803,6 @@ cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int
     }
     if (c.bits == 4) return eight ? launch_rows<64, 4, 1>(p, stream) : launch_rows<64, 4, 2>(p, stream);
     return eight ? launch_rows<64, 8, 1>(p, stream) : launch_rows<64, 8, 2>(p, stream);
-}
-
-cudaError_t read_and_clear_rows_error(int *value)
-{
-    *value = 0;
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_rows_error, sizeof(int));
-    if (e != cudaSuccess) return e;
-    if (v) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_rows_error, &zero, sizeof(int));
-    }
-    *value = v;
-    return e;
 }
 
 }  // namespace qoq
