@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "qoq_attn_internal.h"
+#include "qoq_ptx.cuh"
 
 namespace qoq {
 
@@ -31,6 +32,26 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// wait_bounded() for waits of a microsecond: try_wait without a time hint
+// suspends the thread in hardware and wakes it when the phase completes; the
+// hint adds sleeps and clock reads between tries, which took half of the
+// attention kernel's issue slots.  The clock is looked at every 64 tries.
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t budget_ns)
+{
+    uint64_t start = 0;
+    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries) {
+        if (tries % 64) continue;
+        if (*abort) return false;
+        const uint64_t now = global_timer_ns();
+        if (start == 0) start = now;
+        if (now - start > budget_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 struct TileWork {

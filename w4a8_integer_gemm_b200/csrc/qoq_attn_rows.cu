@@ -173,15 +173,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 {
     using C = RowsCfg<D, BITS, NT>;
     extern __shared__ __align__(128) uint8_t smem[];    // [kWarps][kStages][kStage]
-    __shared__ long long s_sum[kWarps], s_before[kThreads];
+    __shared__ long long s_sum[kWarps], s_before[kThreads], s_run[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const AttnBatch &a = p.a;
     const int capacity = a.table_pages * a.page_size;
     const uint32_t e6 = p.e6, e5 = p.e5;
-    // neighbouring warps of the line sit on different SMs, so that a short line uses all of them
-    const int me = warp * gridDim.x + blockIdx.x;
-
     // the line's length over sequence b; n and grains are set
     auto length_of = [&](int b, int &n, int &grains) -> long long {
         const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
@@ -192,8 +189,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
     };
 
     // ---- this warp's share ----
-    long long at, end, total, ctas;
-    Run run;
+    long long at = 0, end = 0, from = 0, total, ctas;
+    int me;
+    bool neighbours;
+    Run run = {0, 0, 0, 0, 0};
     {
         const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
         long long mine = 0;
@@ -213,12 +212,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             total += s_sum[w];
         }
         s_before[threadIdx.x] = x;
-        if (lane == 0) p.joined[me] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) s_run[warp] = -1;
         __syncthreads();
         grid_launch_dependents();
         ctas = min((long long)gridDim.x * kWarps, (total + kLeast - 1) / kLeast);
-        if (me >= ctas) return;
-        at = total * me / ctas;
+        // the warps of a CTA are neighbours in the line; when it is short they are on different SMs
+        neighbours = ctas == (long long)gridDim.x * kWarps;
+        me = neighbours ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
+        if (lane == 0) p.joined[me] = make_int4(-1, 0, 0, 0);
+        if (me < ctas) {
+        at = from = total * me / ctas;
         end = total * (me + 1) / ctas;
         int lo = 0, hi = kThreads - 1;               // the last thread whose sequences begin at or before `at`
         while (lo < hi) {
@@ -236,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         const int r = (int)(skip / unit);
         run.hk = r % p.Hkv;
         run.row0 = r / p.Hkv * C::kRows;
-        at -= skip % unit;                           // where the run begins; the share begins within it
+        at -= skip % unit;                           // where the run begins; the share begins (`from`) within it
+        }
     }
-    long long from = total * me / ctas;              // where the warp's part of the run begins
     uint8_t *ring_ptr = smem + warp * C::kStages * C::kStage;
     const uint32_t ring = smem_addr(ring_ptr);
     // the lane's parameter of a granule: token lane % 16, of the key or the value
@@ -599,6 +602,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         const bool begins = g0 == 0, ends = g1 == run.grains;
         // a part that began in an earlier warp's share is the warp's first (slot 0), one that goes on its last
         float *part = p.part + ((size_t)me * 2 + (begins ? 1 : 0)) * C::kRows * C::kStride;
+        // a share in the middle of a run: the CTA's warps in that position join their parts first (below)
+        const bool middle = neighbours && !begins && !ends;
+        if (middle) {
+            part = reinterpret_cast<float *>(ring_ptr);
+            if (lane == 0) s_run[warp] = at;
+        }
         const float inv_k = k > 0.0f ? 1.0f / k : 0.0f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -663,83 +672,90 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             }
         }
     }
+    // ---- warps in the middle of one run: their parts become one, the others' are marked empty ----
+    __syncthreads();
+    const long long mine = s_run[warp];
+    if (mine >= 0) {
+        int w0 = warp, w1 = warp + 1;
+        while (w0 > 0 && s_run[w0 - 1] == mine) --w0;
+        while (w1 < kWarps && s_run[w1] == mine) ++w1;
+        float *out = p.part + (size_t)me * 2 * C::kRows * C::kStride;
+        float *first = out - (size_t)(warp - w0) * 2 * C::kRows * C::kStride;   // the first of these warps' part
+        for (int r = warp - w0; r < C::kRows; r += w1 - w0) {
+            float M = -INFINITY, L = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto row = [&](int w) { return reinterpret_cast<const float *>(smem + w * C::kStages * C::kStage) + r * C::kStride; };
+            for (int w = w0; w < w1; ++w) M = fmaxf(M, row(w)[D]);
+            for (int w = w0; w < w1; ++w) {
+                const float m = row(w)[D], f = m == -INFINITY ? 0.0f : exp2_fast(m - M);
+                L = fmaf(row(w)[D + 1], f, L);
+                if (lane < D / 4) {
+                    const float4 y = reinterpret_cast<const float4 *>(row(w))[lane];
+                    v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
+                }
+            }
+            if (lane < D / 4) reinterpret_cast<float4 *>(first + r * C::kStride)[lane] = v;
+            if (lane == 0) *reinterpret_cast<float2 *>(first + r * C::kStride + D) = make_float2(M, L);
+        }
+        if (warp > w0 && lane < C::kRows) *reinterpret_cast<float2 *>(out + lane * C::kStride + D) = make_float2(-INFINITY, 0.0f);
+    }
 }
 
-// Joins the runs that span warps.  CTA (x, y) looks at eight warps' ends and
-// takes rows 2y and 2y + 1 of each run that ended there; eight of its 16
-// warps share a row's parts, four in flight at a time, and the sums are
-// joined in order.  A lane holds D / 32 channels.
-constexpr int kJoinThreads = 512;
-
+// Joins the runs that span warps: CTA x the run that ended in warp x's share,
+// one row per warp.  The lanes weigh 32 parts at a time; then the warp adds
+// those that are not empty, in order, a lane holding four channels.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const RowsArgs p)
+__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs p)
 {
-    constexpr int kRows = 8 * NT, kStride = D + 4, kN = D / 32;
-    __shared__ float s_v[2][8][D];
-    __shared__ float2 s_ml[2][8];
+    constexpr int kRows = 8 * NT, kStride = D + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = warp >> 3, w8 = warp & 7;
     grid_dependency_wait();
-    for (int e = 0; e < 8; ++e) {
-        const int last = blockIdx.x * 8 + e;
-        const int4 j = p.joined[last];
-        if (j.x < 0) continue;
-        const int t_seq = __ldg(p.a.cu + j.x), n = __ldg(p.a.cu + j.x + 1) - t_seq, rows = min(kRows, n * p.G - j.y);
-        const int row = 2 * blockIdx.y + half;
-        if (2 * (int)blockIdx.y >= rows) continue;           // the same for the whole CTA
-        float v[kN], M = -INFINITY, L = 0.0f;
+    const int last = blockIdx.x;
+    const int4 j = p.joined[last];
+    if (j.x < 0) return;
+    const int t_seq = __ldg(p.a.cu + j.x), n = __ldg(p.a.cu + j.x + 1) - t_seq, rows = min(kRows, n * p.G - j.y);
+    for (int row = warp; row < rows; row += kWarps) {
+        const float *parts = p.part + row * kStride;
+        auto part = [&](int w) { return parts + ((size_t)w * 2 + (w == j.w ? 1 : 0)) * kRows * kStride; };
+        float M = -INFINITY, L = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w0 = j.w; w0 <= last; w0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (w0 + lane <= last) ml = *reinterpret_cast<const float2 *>(part(w0 + lane) + D);
+            const float m1 = fmaxf(M, warp_max(ml.x));
+            if (m1 == -INFINITY) continue;
+            const float f0 = M == -INFINITY ? 0.0f : exp2_fast(M - m1);
+            const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m1);
+            float l = ml.y * f;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = 0.0f;
-        if (row < rows) {
-            for (int w = j.w + w8; w <= last; w += 32) {
-                float y[4][kN];
-                float2 ml[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    ml[u] = make_float2(-INFINITY, 0.0f);
-                    if (w + 8 * u > last) continue;
-                    const float *x = p.part + (((size_t)(w + 8 * u) * 2 + (w + 8 * u == j.w ? 1 : 0)) * kRows + row) * kStride;
-                    ml[u] = *reinterpret_cast<const float2 *>(x + D);
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) y[u][i] = x[32 * i + lane];
-                }
-                const float m1 = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-                if (m1 == -INFINITY) continue;
-                const float f0 = M == -INFINITY ? 0.0f : exp2_fast(M - m1);
-                M = m1;
-                L *= f0;
-#pragma unroll
-                for (int i = 0; i < kN; ++i) v[i] *= f0;
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            M = m1;
+            L = fmaf(L, f0, l);
+            v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+            uint32_t todo = __ballot_sync(0xffffffffu, f > 0.0f);
+            while (todo) {
+                float4 y[4];
+                float g[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    if (ml[u].x == -INFINITY) continue;
-                    const float f = exp2_fast(ml[u].x - m1);
-                    L = fmaf(ml[u].y, f, L);
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) v[i] = fmaf(y[u][i], f, v[i]);
+                    const int i = todo ? __ffs(todo) - 1 : 0;
+                    g[u] = todo ? __shfl_sync(0xffffffffu, f, i) : 0.0f;
+                    y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (todo && lane < D / 4) y[u] = reinterpret_cast<const float4 *>(part(w0 + i))[lane];
+                    todo &= todo - 1;
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v = make_float4(fmaf(y[u].x, g[u], v.x), fmaf(y[u].y, g[u], v.y), fmaf(y[u].z, g[u], v.z),
+                                    fmaf(y[u].w, g[u], v.w));
             }
         }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) s_v[half][w8][32 * i + lane] = v[i];
-        if (lane == 0) s_ml[half][w8] = make_float2(M, L);
-        __syncthreads();
-        for (int x = threadIdx.x; x < 2 * D; x += kJoinThreads) {
-            const int hf = x / D, ch = x % D, r = j.y + 2 * blockIdx.y + hf;
-            if (2 * (int)blockIdx.y + hf >= rows) continue;
-            float m = -INFINITY, l = 0.0f, o = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, s_ml[hf][w].x);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float f = s_ml[hf][w].x == -INFINITY ? 0.0f : exp2_fast(s_ml[hf][w].x - m);
-                l = fmaf(s_ml[hf][w].y, f, l);
-                o = fmaf(s_v[hf][w][ch], f, o);
-            }
-            p.out[(int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + ch] =
-                float_to_half_bits(l > 0.0f ? o / l : 0.0f);
-        }
-        __syncthreads();
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const int r = j.y + row;
+        const __half2 h0 = __floats2half2_rn(v.x * inv, v.y * inv), h1 = __floats2half2_rn(v.z * inv, v.w * inv);
+        if (lane < D / 4)
+            *reinterpret_cast<uint2 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo + (size_t)(j.z * p.G + r % p.G) * D + 4 * lane) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
     }
 }
 
@@ -771,8 +787,8 @@ cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // the join's CTAs come up while the first kernel runs and wait for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas * kWarps / 8, 4 * NT);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(ctas * kWarps);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -31,6 +31,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "qoq_attn_internal.h"
 #include "qoq_attn_device.cuh"
@@ -77,6 +78,33 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two FP32 numbers in a register pair, and the instructions that work on both.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // byte offset of 16-byte vector `vec` of row `row` in a [rows][64 channels] block, 128-byte swizzle
@@ -208,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             };
             // ring items: K of step i is item 2i, V is item 2i + 1
             auto ready = [&](int item) {
-                return wait_bounded(full(item % C::kSlots), (uint32_t)(item / C::kSlots) & 1, &abort_flag, kBudgetNs);
+                return wait_short(full(item % C::kSlots), (uint32_t)(item / C::kSlots) & 1, &abort_flag, kBudgetNs);
             };
             bool ok = ready(0);
             if (ok) {
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
                 ok = ready(vi) && (i + 1 >= steps || ready(ki));
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (i >= cnt[t]) continue;
-                    ok = wait_bounded(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs);
+                    ok = wait_short(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs);
                     if (!ok) break;
                     tc_fence_after();
                     values(t, vi % C::kSlots, i > 0);
@@ -248,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
         const int items = 2 * steps;
         auto slot_free = [&](int item) {
             if (item < C::kSlots) return true;
-            return (bool)__all_sync(0xffffffffu, wait_bounded(empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1,
+            return (bool)__all_sync(0xffffffffu, wait_short(empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1,
                                                               &abort_flag, kBudgetNs));
         };
         auto signal = [&](int item) {
@@ -257,24 +285,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             if (lane == 0) mbar_arrive(full(item % C::kSlots));
         };
         if (BITS == 0) {
-            constexpr int kVecs = D / 8, kPass = 128 / kVecs;        // rows a pass of the 128 threads covers
+            constexpr int kVecs = D / 8, kPass = 128 / kVecs;        // rows a pass of the 128 threads covers: 8 or 16,
+                                                                     // so the swizzle of a thread's rows is one number
             constexpr int kLag = 2;                                  // items in flight behind the newest
             const int vec = tid % kVecs, r0 = tid / kVecs;
+            const uint32_t my_dst = sbase + C::kRing + (vec >> 3) * C::kBlock + swz(r0, vec);
+            const uint16_t *kp = p.k + (int64_t)(t_seq + j0 * kKeys + r0) * p.ldk + (size_t)hk * D + vec * 8;
+            const uint16_t *vp = p.v + (int64_t)(t_seq + j0 * kKeys + r0) * p.ldv + (size_t)hk * D + vec * 8;
+            const int64_t k_pass = p.ldk * kPass, v_pass = p.ldv * kPass;
             bool ok = true;
             for (int item = 0; item < items + kLag; ++item) {
                 if (item < items) {
                     ok = slot_free(item);
                     if (!ok) break;
                     const bool val = item & 1;
-                    const int key0 = (j0 + (item >> 1)) * kKeys;
-                    const int64_t ld = val ? p.ldv : p.ldk;
-                    const uint16_t *src = (val ? p.v : p.k) + (int64_t)(t_seq + key0) * ld + (size_t)hk * D + vec * 8;
-                    const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile + (vec >> 3) * C::kBlock;
+                    const int left = n - (j0 + (item >> 1)) * kKeys - r0;    // rows past the sequence are zeros
+                    const uint16_t *src = val ? vp : kp;
+                    const int64_t pass = val ? v_pass : k_pass;
+                    const uint32_t dst = my_dst + (item % C::kSlots) * C::kTile;
+                    if (left >= kKeys - r0) {
+#pragma unroll
+                        for (int i = 0; i < kKeys / kPass; ++i, src += pass) cp_async<16>(dst + i * kPass * 128, src);
+                    } else {
 #pragma unroll 4
-                    for (int r = r0; r < kKeys; r += kPass) {
-                        const bool in = key0 + r < n;                // rows past the sequence are zeros
-                        cp_async16(dst + swz(r, vec), in ? src + (int64_t)r * ld : src, in);
+                        for (int i = 0; i < kKeys / kPass; ++i, src += pass)
+                            cp_async16(dst + i * kPass * 128, i * kPass < left ? src : p.k, i * kPass < left);
                     }
+                    (val ? vp : kp) += (val ? p.ldv : p.ldk) * kKeys;
                 }
                 cp_async_commit();
                 if (item >= kLag) {
@@ -374,58 +411,79 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             // (cache) which 16-token pieces of the tile are there
             uint32_t there = 0xFFu;
             if (BITS) there = __ballot_sync(0xffffffffu, lane < 8 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
-            ok = __all_sync(0xffffffffu, wait_bounded(sfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs));
+            ok = __all_sync(0xffffffffu, wait_short(sfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs));
             if (!ok) break;
             tc_fence_after();
-            float s[kKeys];
-            tmem_ld64(ts, reinterpret_cast<uint32_t *>(s));
-            tmem_ld64(ts + 64, reinterpret_cast<uint32_t *>(s) + 64);
-            if (see_min < key0 + kKeys || there != 0xFFu) {
-                const int lim = see - key0;
+            const int lim = see - key0;
+            auto softmax = [&](auto masked) {
+                // -inf over the columns [c0, c0 + n) of x that the row does not see
+                auto mask = [&](uint32_t *x, int c0, int n) {
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    if (c >= lim || !((there >> (c >> 4)) & 1)) s[c] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+                    for (int c = 0; c < n; ++c)
+                        if (c0 + c >= lim || !((there >> ((c0 + c) >> 4)) & 1)) x[c] = 0xFF800000u;
+                };
+                // pass 1: the row's maximum.  S is read from tensor memory twice, 32 columns at a time (a read costs
+                // little, and a whole row in registers costs moves and spills)
+                float top = -INFINITY;
 #pragma unroll
-            for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-            // The maximum in use lags behind by up to 2^8: weights stay below 2^8 (FP16 holds 2^15), and O is
-            // rescaled rarely instead of in every tile.
-            const bool grow = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float m1 = grow ? top : m;
-                const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
-                m = m1;
-                l *= keep;
-                if (i > 0) {
-                    // S of this step is complete, so is P V of the last one (issued before it)
+                for (int c0 = 0; c0 < kKeys; c0 += 64) {
+                    uint32_t x[64];
+                    tmem_ld32x2(ts + c0, ts + c0 + 32, x, x + 32);
+                    if (masked.value) mask(x, c0, 64);
+                    float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c, o);
+                    for (int c = 0; c < 64; c += 2)
+                        mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
+                top *= sl;
+                // The maximum in use lags behind by up to 2^8: weights stay below 2^8 (FP16 holds 2^15), and O is
+                // rescaled rarely instead of in every tile.
+                const bool grow = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float m1 = grow ? top : m;
+                    const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
+                    m = m1;
+                    l *= keep;
+                    if (i > 0) {
+                        // S of this step is complete, so is P V of the last one (issued before it)
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-                        tmem_st32(to + c, o);
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, o);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                            tmem_st32(to + c, o);
+                        }
                     }
                 }
-            }
-            const float sub = m == -INFINITY ? 0.0f : m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                // pass 2: P = 2^(s - m), FP16, over the columns of S already read
+                const float sub = m == -INFINITY ? 0.0f : -m;
+                const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int c0 = 0; c0 < kKeys; c0 += 64) {
-                uint32_t pk[32];
+                for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                    uint32_t x[32], pk[16];
+                    tmem_ld32(ts + c0, x);
+                    if (masked.value) mask(x, c0, 32);
 #pragma unroll
-                for (int u = 0; u < 32; ++u) {
-                    const float a = ex2(fmaf(s[c0 + 2 * u], sl, -sub)), b = ex2(fmaf(s[c0 + 2 * u + 1], sl, -sub));
-                    sum[2 * (u & 1)] += a;
-                    sum[2 * (u & 1) + 1] += b;
-                    const __half2 h = __floats2half2_rn(a, b);
-                    pk[u] = *reinterpret_cast<const uint32_t *>(&h);
+                    for (int u = 0; u < 16; ++u) {
+                        float a, b;
+                        unpair(fma2(pair(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), sl2, sub2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[u & 1] = add2(sum[u & 1], pair(a, b));
+                        const __half2 h = __floats2half2_rn(a, b);
+                        pk[u] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    tmem_st16(ts + c0 / 2, pk);
                 }
-                tmem_st32(ts + c0 / 2, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float a, b;
+                unpair(add2(sum[0], sum[1]), a, b);
+                l += a + b;
+            };
+            if (see_min < key0 + kKeys || there != 0xFFu) softmax(std::true_type{});
+            else softmax(std::false_type{});
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -433,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
         }
         // ---- O out ----
         if (ok && cnt[t] > 0) {
-            ok = __all_sync(0xffffffffu, wait_bounded(ofull(t), 0, &abort_flag, kBudgetNs));
+            ok = __all_sync(0xffffffffu, wait_short(ofull(t), 0, &abort_flag, kBudgetNs));
             tc_fence_after();
         }
         if (ok) {
