@@ -142,30 +142,37 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 x)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
 // Eight 4-bit codes -> fp16(s c + m) of channels 0 4, 1 5, 2 6, 3 7.  A
 // nibble in bits 0-3 under the exponent of 1024 is 1024 + c, in bits 4-7
 // under that of 64 it is 64 + c (the mantissa's unit is 2^-4 there): one
 // logic operation and one exact subtraction give c, one multiply-add rounds
-// once.  par: (s, m).
-__device__ __forceinline__ uint4 expand4(uint32_t x, uint32_t par)
+// once.  par: (s, m).  The exponent patterns e6 = 0x64006400 and e5 =
+// 0x54005400 come in registers whose values the compiler does not know: a
+// logic instruction has room for one constant, and with two it becomes two.
+__device__ __forceinline__ uint4 expand4(uint32_t x, uint32_t par, uint32_t e6, uint32_t e5)
 {
     const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
     const uint32_t y = x >> 8;
-    const uint32_t a = sub_h2((x & 0x000F000Fu) | 0x64006400u, 0x64006400u);
-    const uint32_t b = sub_h2((x & 0x00F000F0u) | 0x54005400u, 0x54005400u);
-    const uint32_t c = sub_h2((y & 0x000F000Fu) | 0x64006400u, 0x64006400u);
-    const uint32_t d = sub_h2((y & 0x00F000F0u) | 0x54005400u, 0x54005400u);
+    const uint32_t a = sub_h2((x & 0x000F000Fu) | e6, 0x64006400u);
+    const uint32_t b = sub_h2((x & 0x00F000F0u) | e5, 0x54005400u);
+    const uint32_t c = sub_h2((y & 0x000F000Fu) | e6, 0x64006400u);
+    const uint32_t d = sub_h2((y & 0x00F000F0u) | e5, 0x54005400u);
     return make_uint4(fma_h2(a, s, m), fma_h2(b, s, m), fma_h2(c, s, m), fma_h2(d, s, m));
 }
 
 // Eight 8-bit codes (x: channels 0-3, y: 4-7) -> fp16(s c + m), in order.
-__device__ __forceinline__ uint4 expand8(uint32_t x, uint32_t y, uint32_t par)
+__device__ __forceinline__ uint4 expand8(uint32_t x, uint32_t y, uint32_t par, uint32_t e6)
 {
     const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
-    const uint32_t a = sub_h2(__byte_perm(x, 0x64646464u, 0x4140), 0x64006400u);
-    const uint32_t b = sub_h2(__byte_perm(x, 0x64646464u, 0x4342), 0x64006400u);
-    const uint32_t c = sub_h2(__byte_perm(y, 0x64646464u, 0x4140), 0x64006400u);
-    const uint32_t d = sub_h2(__byte_perm(y, 0x64646464u, 0x4342), 0x64006400u);
+    const uint32_t a = sub_h2(__byte_perm(x, e6, 0x5150), 0x64006400u);
+    const uint32_t b = sub_h2(__byte_perm(x, e6, 0x5352), 0x64006400u);
+    const uint32_t c = sub_h2(__byte_perm(y, e6, 0x5150), 0x64006400u);
+    const uint32_t d = sub_h2(__byte_perm(y, e6, 0x5352), 0x64006400u);
     return make_uint4(fma_h2(a, s, m), fma_h2(b, s, m), fma_h2(c, s, m), fma_h2(d, s, m));
 }
 

@@ -14,10 +14,10 @@
 //                    tensor memory over S; rescale O (tensor memory) when
 //                    the maximum grew by more than 2^8; at the end O to HBM.
 //   warps 8-11       loader: keys and values of the tile into a ring of
-//                    shared-memory slots in the 128-byte-swizzled layout:
-//                    cp.async for FP16 rows, or the codes expanded to
-//                    fp16(s c + m) in registers.
-//   warp 12          one thread issues the MMAs: S = Q K^T (both from shared
+//                    shared-memory slots in the 128-byte-swizzled layout: TMA
+//                    for FP16 rows; for a cache the codes, expanded to
+//                    fp16(s c + m) in registers (keys; warps 12-15 values).
+//   the last         one thread issues the MMAs: S = Q K^T (both from shared
 //                    memory), O += P V (P from tensor memory, V with its
 //                    channels contiguous).
 // Tensor memory: S0 S1 (128 columns each, P over the first half), O0 O1 (D
@@ -27,10 +27,12 @@
 // each weight; the sum of weights is taken before it, in FP32) and, for a
 // cache, the expanded keys and values (half a step, against a quantisation
 // step of 1/15 or 1/255 of the row's range).
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "qoq_attn_internal.h"
@@ -41,7 +43,8 @@
 namespace qoq {
 namespace {
 
-constexpr int kThreads = 512;
+// Threads: two softmax warpgroups, one loader (TMA) or two (keys, values of a cache), and the MMA issuer's.
+__host__ __device__ constexpr int tile_threads(int bits) { return bits ? 640 : 512; }
 constexpr int kRows = 256;          // rows of a CTA (two tiles of 128)
 constexpr int kKeys = 128;          // keys of a tile
 constexpr uint32_t kNone = 0xFFFFFFFFu;
@@ -71,6 +74,8 @@ struct TileArgs {
     int few;                // sequences with at most this many rows (n_b * G) are another kernel's
     float scale_log2;       // |scale| * log2(e)
     uint32_t flip;          // 0x80008000 when scale < 0: the sign goes into q
+    uint32_t e6, e5;        // 0x64006400, 0x54005400 (expand4)
+    CUtensorMap map_k, map_v;   // (prompts) [T][Hkv * D], boxes of 64 channels x 128 rows, 128-byte swizzle
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -107,6 +112,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// 2^x of two numbers below 2^7 on the FMA pipe: 2^x = 2^n 2^f with n = round(x) (adding 1.5 * 2^23 leaves n in the
+// low bits), 2^f on [-1/2, 1/2] by the cubic of least relative error, 7.5e-5 (found by linear programming; P is
+// rounded to FP16, 4.9e-4, next).  Below 2^-126 the result is some number below 2^-125.
+__device__ __forceinline__ void ex2_pair(float &x, float &y)
+{
+    const uint64_t t = pair(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
+    const uint64_t r = add2(t, pair(12582912.0f, 12582912.0f));
+    const uint64_t f = add2(t, fma2(r, pair(-1.0f, -1.0f), pair(12582912.0f, 12582912.0f)));
+    uint64_t p = fma2(f, pair(0.0551716685f, 0.0551716685f), pair(0.242611125f, 0.242611125f));
+    p = fma2(p, f, pair(0.693260968f, 0.693260968f));
+    p = fma2(p, f, pair(0.999928057f, 0.999928057f));
+    float n0, n1;
+    unpair(r, n0, n1);
+    unpair(p, x, y);
+    x = __uint_as_float(__float_as_uint(x) + (__float_as_uint(n0) << 23));
+    y = __uint_as_float(__float_as_uint(y) + (__float_as_uint(n1) << 23));
+}
+
+// Pairs of every 8 whose exponential runs on the FMA pipe: the other pipe makes four a clock and SM quarter, which
+// alone would take as long as the tensor cores take for the tile.
+constexpr int kPoly = 3;
+
 // byte offset of 16-byte vector `vec` of row `row` in a [rows][64 channels] block, 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int row, int vec)
 {
@@ -125,15 +152,20 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Registers: launched with 512 x 128; 2 x 128 x 184 + 128 x 96 + 128 x 48 = 512 x 128.
-constexpr int kRegsSoftmax = 184, kRegsLoader = 96, kRegsMma = 48;
-static_assert(256 * kRegsSoftmax + 128 * kRegsLoader + 128 * kRegsMma <= kThreads * 128, "register split");
+// Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 512 with 128.
+template <int BITS>
+struct Regs {
+    static constexpr int kSoftmax = BITS ? 120 : 152, kLoader = BITS ? 88 : 72, kMma = BITS ? 64 : 80;
+    static constexpr int kLoaders = BITS ? 2 : 1;
+    static_assert(256 * kSoftmax + 128 * (kLoaders * kLoader + kMma) <= tile_threads(BITS) * (BITS ? 96 : 128), "register split");
+};
 
 // BITS 0: FP16 rows of the batch itself (prompts); 4 or 8: the cache.
 template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p)
+__global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const __grid_constant__ TileArgs p)
 {
     using C = TileCfg<D>;
+    constexpr int kThreads = tile_threads(BITS), kMmaWarp = kThreads / 32 - 4;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -187,10 +219,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
         abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(&tmem_slot), 512);
         tmem_relinquish();
     }
+    // A warpgroup's wait: one warp polls, the others sleep in a named barrier instead of polling too.
+    auto group_wait = [&](int id, bool polls, uint32_t bar, uint32_t parity) -> bool {
+        if (polls) wait_short(bar, parity, &abort_flag, kBudgetNs);
+        named_barrier(id, 128);
+        return !*(volatile int *)&abort_flag;
+    };
     // ---- Q: 256 rows into shared memory, zeros past the end ----
     if (steps > 0) {
         for (int e = threadIdx.x; e < kRows * (D / 8); e += kThreads) {
@@ -212,27 +250,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    if (warp >= 12) {
+    if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA --
-        regs_down<kRegsMma>();
-        if (warp == 12 && lane == 0 && steps > 0) {
+        regs_down<Regs<BITS>::kMma>();
+        if (warp == kMmaWarp && lane == 0 && steps > 0) {
             const uint32_t is = idesc_f16_m128(kKeys, false), io = idesc_f16_m128(D, true);
+            const uint32_t q_lo = desc_sw128_lo(sbase + C::kQ, 1), k_lo = desc_sw128_lo(sbase + C::kRing, 1);
+            const uint32_t v_lo = desc_sw128_lo(sbase + C::kRing, C::kBlock >> 4);
             auto scores = [&](int t, int slot) {
+                const uint32_t qa = q_lo + t * (C::kTile >> 4), kb = k_lo + slot * (C::kTile >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kBlock;
-                    const uint64_t qa = smem_desc_sw128(sbase + C::kQ + t * C::kTile + off) + 2 * (kk & 3);
-                    const uint64_t kb = smem_desc_sw128(sbase + C::kRing + slot * C::kTile + off) + 2 * (kk & 3);
-                    mma_f16_ss(tmem + 128 * t, qa, kb, is, kk > 0);
+                    const uint32_t off = (kk >> 2) * (C::kBlock >> 4) + 2 * (kk & 3);
+                    mma_f16_ss(tmem + 128 * t, qa + off, kb + off, kDescSw128Hi, kDescSw128Hi, is, kk > 0);
                 }
                 mma_commit(sfull(t));
             };
             auto values = [&](int t, int slot, bool accumulate) {
+                const uint32_t vb = v_lo + slot * (C::kTile >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk) {
-                    const uint64_t vb = smem_desc_sw128_mn(sbase + C::kRing + slot * C::kTile + kk * 2048, C::kBlock);
-                    mma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, vb, io, accumulate || kk > 0);
-                }
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, vb + 128 * kk, kDescSw128Hi, io,
+                               accumulate || kk > 0);
             };
             // ring items: K of step i is item 2i, V is item 2i + 1
             auto ready = [&](int item) {
@@ -247,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             }
             for (int i = 0; i < steps && ok; ++i) {
                 const int vi = 2 * i + 1, ki = 2 * i + 2;
-                ok = ready(vi) && (i + 1 >= steps || ready(ki));
+                bool have_k = false;
+                ok = ready(vi);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (i >= cnt[t]) continue;
                     ok = wait_short(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs);
@@ -255,8 +295,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
                     tc_fence_after();
                     values(t, vi % C::kSlots, i > 0);
                     // S of the next step goes over P of this one: MMAs run in the order they were issued
-                    if (i + 1 < cnt[t]) scores(t, ki % C::kSlots);
-                    else mma_commit(ofull(t));
+                    if (i + 1 < cnt[t]) {
+                        if (!have_k) {
+                            ok = have_k = ready(ki);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        scores(t, ki % C::kSlots);
+                    } else {
+                        mma_commit(ofull(t));
+                    }
                 }
                 if (!ok) break;
                 mma_commit(empty(vi % C::kSlots));
@@ -271,13 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
         }
     } else if (warp >= 8) {
         // --------------------------------------------------------- loader --
-        regs_down<kRegsLoader>();
-        const int tid = threadIdx.x - 256;
+        regs_down<Regs<BITS>::kLoader>();
         const int items = 2 * steps;
         auto slot_free = [&](int item) {
             if (item < C::kSlots) return true;
             return (bool)__all_sync(0xffffffffu, wait_short(empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1,
-                                                              &abort_flag, kBudgetNs));
+                                                            &abort_flag, kBudgetNs));
         };
         auto signal = [&](int item) {
             fence_proxy_async_smem();
@@ -285,116 +332,121 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             if (lane == 0) mbar_arrive(full(item % C::kSlots));
         };
         if (BITS == 0) {
-            constexpr int kVecs = D / 8, kPass = 128 / kVecs;        // rows a pass of the 128 threads covers: 8 or 16,
-                                                                     // so the swizzle of a thread's rows is one number
-            constexpr int kLag = 2;                                  // items in flight behind the newest
-            const int vec = tid % kVecs, r0 = tid / kVecs;
-            const uint32_t my_dst = sbase + C::kRing + (vec >> 3) * C::kBlock + swz(r0, vec);
-            const uint16_t *kp = p.k + (int64_t)(t_seq + j0 * kKeys + r0) * p.ldk + (size_t)hk * D + vec * 8;
-            const uint16_t *vp = p.v + (int64_t)(t_seq + j0 * kKeys + r0) * p.ldv + (size_t)hk * D + vec * 8;
-            const int64_t k_pass = p.ldk * kPass, v_pass = p.ldv * kPass;
-            bool ok = true;
-            for (int item = 0; item < items + kLag; ++item) {
-                if (item < items) {
-                    ok = slot_free(item);
-                    if (!ok) break;
-                    const bool val = item & 1;
-                    const int left = n - (j0 + (item >> 1)) * kKeys - r0;    // rows past the sequence are zeros
-                    const uint16_t *src = val ? vp : kp;
-                    const int64_t pass = val ? v_pass : k_pass;
-                    const uint32_t dst = my_dst + (item % C::kSlots) * C::kTile;
-                    if (left >= kKeys - r0) {
+            // TMA, issued by one thread, except for the last values of a sequence: rows behind it are another's, or
+            // nobody's, and may hold anything, and a weight of zero does not silence an infinity.  (Keys there only
+            // make scores that are masked.)
+            const int tid = threadIdx.x - 256;
+            const bool ragged = steps > 0 && (j0 + steps) * kKeys > n;
+            if (warp == 8) {
+                for (int item = 0; item < items - (ragged ? 1 : 0); ++item) {
+                    if (!slot_free(item)) break;
+                    if (lane == 0) {
+                        const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile, bar = full(item % C::kSlots);
+                        mbar_arrive_expect_tx(bar, C::kTile);
+                        mbar_arrive_n(bar, 3);
 #pragma unroll
-                        for (int i = 0; i < kKeys / kPass; ++i, src += pass) cp_async<16>(dst + i * kPass * 128, src);
-                    } else {
-#pragma unroll 4
-                        for (int i = 0; i < kKeys / kPass; ++i, src += pass)
-                            cp_async16(dst + i * kPass * 128, i * kPass < left ? src : p.k, i * kPass < left);
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            tma_load_2d(dst + blk * C::kBlock, item & 1 ? &p.map_v : &p.map_k, hk * D + 64 * blk,
+                                        t_seq + (j0 + (item >> 1)) * kKeys, bar);
                     }
-                    (val ? vp : kp) += (val ? p.ldv : p.ldk) * kKeys;
                 }
-                cp_async_commit();
-                if (item >= kLag) {
-                    cp_async_wait<kLag>();
-                    signal(item - kLag);
+                if (ragged) slot_free(items - 1);
+            }
+            if (ragged) {
+                named_barrier(1, 128);
+                if (!*(volatile int *)&abort_flag) {
+                    constexpr int kVecs = D / 8, kPass = 128 / kVecs;
+                    const int vec = tid % kVecs, item = items - 1, key0 = (j0 + steps - 1) * kKeys;
+                    const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile + (vec >> 3) * C::kBlock;
+                    for (int r = tid / kVecs; r < kKeys; r += kPass) {
+                        const bool in = key0 + r < n;
+                        cp_async16(dst + swz(r, vec),
+                                   in ? p.v + (int64_t)(t_seq + key0 + r) * p.ldv + (size_t)hk * D + vec * 8 : p.v, in);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    signal(item);
                 }
             }
-            cp_async_wait<0>();
         } else {
-            // Lanes share a row's bytes, 16 each; a thread's rows are kPass apart.
+            // One warpgroup brings the keys, the other the values.  kLanes lanes share a row's bytes, 16 each; a thread's
+            // kLanes rows lie in one granule of 16 tokens, kGap apart, so one page and constant offsets serve them.
             constexpr int kB = BITS ? BITS : 4;
-            constexpr int kRowBytes = D * kB / 8, kLanes = kRowBytes / 16, kPass = 128 / kLanes, kN = kKeys / kPass;
-            const int part = tid % kLanes, r0 = tid / kLanes;
-            uint4 kc[kN], vc[kN];
-            uint32_t kp[kN], vp[kN];
-            uint32_t at[kN];                                         // cache row of the thread's keys (a pool of 2^32 rows
-                                                                     // would not fit the GPU), or kNone
-            auto locate = [&](int step) {
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const int pos = (j0 + step) * kKeys + r0 + i * kPass;
-                    const int page = pos < first + n ? page_of(p.a, w.b, pos) : -1;
-                    at[i] = page < 0 ? kNone
-                                     : ((uint32_t)page * p.Hkv + hk) * p.a.page_size + (pos & (p.a.page_size - 1));
-                }
+            constexpr int kRowBytes = D * kB / 8, kLanes = kRowBytes / 16, kGap = 16 / kLanes;
+            constexpr int kVecs = 128 / kB / 8;                      // 16-byte vectors of 8 channels from 16 bytes of codes
+            const bool val = warp >= 12;
+            const int tid = threadIdx.x & 127, part = tid % kLanes;
+            const int r0 = 16 * (tid / 16) + tid % 16 / kLanes;      // r0 % 8 is below kGap, and the other rows' r % 8 are
+                                                                     // r0 % 8 ^ (kGap i % 8)
+            const uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + part * 16;
+            const uint32_t *pars = reinterpret_cast<const uint32_t *>(val ? p.c.v_par : p.c.k_par);
+            const int end = first + n;
+            uint4 c[kLanes];
+            uint32_t pr[kLanes];
+            int page = -1;                                           // of the next step to be fetched
+            auto look_up = [&](int step) {
+                const int pos = (j0 + step) * kKeys + r0;
+                page = (pos & ~15) < end ? page_of(p.a, w.b, pos) : -1;
             };
-            auto fetch = [&](uint4 (&c)[kN], uint32_t (&pr)[kN], const uint8_t *codes, const uint16_t *par) {
+            auto fetch = [&](int step) {
+                const int pos = (j0 + step) * kKeys + r0;
+                // (a pool of 2^32 rows would not fit the GPU)
+                const uint32_t row = ((uint32_t)page * p.Hkv + hk) * p.a.page_size + (pos & (p.a.page_size - 1));
+                const uint8_t *src = codes + (size_t)row * kRowBytes;
+                const uint32_t *par = pars + row;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
+                for (int i = 0; i < kLanes; ++i) {
                     c[i] = make_uint4(0, 0, 0, 0);
                     pr[i] = 0;
-                    if (at[i] != kNone) {
-                        c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)at[i] * kRowBytes) + part);
-                        pr[i] = __ldg(reinterpret_cast<const uint32_t *>(par) + at[i]);
+                    if (page >= 0 && pos + kGap * i < end) {         // what nobody sees becomes zeros
+                        c[i] = __ldg(reinterpret_cast<const uint4 *>(src + kGap * i * kRowBytes));
+                        pr[i] = __ldg(par + kGap * i);
                     }
                 }
+                look_up(step + 1);
             };
-            auto expand = [&](int item, const uint4 (&c)[kN], const uint32_t (&pr)[kN]) {
-                uint8_t *dst = smem + C::kRing + (item % C::kSlots) * C::kTile;
+            // Vector v of the thread's codes is vector kVecs * part + v of the row.  Lanes of the row's upper half store
+            // theirs in another order, so that eight lanes meet eight bank groups.
+            const int twist = D == 128 && part >= kLanes / 2 ? kVecs / 2 : 0;
+            uint32_t at[kVecs];
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const int r = r0 + i * kPass;
+            for (int u = 0; u < kVecs; ++u) {
+                const int vec = kVecs * part + (u ^ twist);
+                at[u] = (uint32_t)((vec >> 3) * C::kBlock) + swz(r0, vec);
+            }
+            auto expand = [&](int item) {
+                const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile;
+#pragma unroll
+                for (int i = 0; i < kLanes; ++i) {
                     const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-                    if (kB == 4) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            // the upper lanes of a row store in another order: eight lanes, eight bank groups
-                            const bool other = D == 128 && (part & 2);
-                            const int vec = 4 * part + (other ? u ^ 2 : u);
-                            *reinterpret_cast<uint4 *>(dst + (vec >> 3) * C::kBlock + swz(r, vec)) =
-                                expand4(other ? cw[u ^ 2] : cw[u], pr[i]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const bool other = D == 128 && (part & 4);
-                            const int vec = 2 * part + (other ? u ^ 1 : u);
-                            *reinterpret_cast<uint4 *>(dst + (vec >> 3) * C::kBlock + swz(r, vec)) =
-                                expand8(other ? cw[2 * (u ^ 1)] : cw[2 * u], other ? cw[2 * (u ^ 1) + 1] : cw[2 * u + 1], pr[i]);
-                        }
+                    for (int u = 0; u < kVecs; ++u) {
+                        constexpr int kHalf = kVecs / 2;
+                        uint4 x;
+                        if (kB == 4) x = expand4(twist ? cw[u ^ kHalf] : cw[u], pr[i], p.e6, p.e5);
+                        else x = expand8(twist ? cw[2 * (u ^ kHalf) % 4] : cw[2 * u % 4],
+                                         twist ? cw[(2 * (u ^ kHalf) + 1) % 4] : cw[(2 * u + 1) % 4], pr[i], p.e6);
+                        st_shared16(dst + (at[u] ^ ((kGap * i & 7) << 4)) + kGap * i * 128, x);
                     }
                 }
             };
             if (steps > 0) {
-                locate(0);
-                fetch(kc, kp, p.c.k_codes, p.c.k_par);
-                fetch(vc, vp, p.c.v_codes, p.c.v_par);
+                look_up(0);
+                fetch(0);
             }
             for (int i = 0; i < steps; ++i) {
-                if (i + 1 < steps) locate(i + 1);
-                if (!slot_free(2 * i)) break;
-                expand(2 * i, kc, kp);
-                signal(2 * i);
-                if (i + 1 < steps) fetch(kc, kp, p.c.k_codes, p.c.k_par);
-                if (!slot_free(2 * i + 1)) break;
-                expand(2 * i + 1, vc, vp);
-                signal(2 * i + 1);
-                if (i + 1 < steps) fetch(vc, vp, p.c.v_codes, p.c.v_par);
+                const int item = 2 * i + val;
+                if (item >= C::kSlots &&
+                    !group_wait(4 + val, (warp & 3) == 0, empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1))
+                    break;
+                expand(item);
+                signal(item);
+                if (i + 1 < steps) fetch(i + 1);
             }
         }
     } else {
         // -------------------------------------------------------- softmax --
-        regs_up<kRegsSoftmax>();
+        regs_up<Regs<BITS>::kSoftmax>();
         const int t = warp >> 2, r = (warp & 3) * 32 + lane;         // row tile, row of it
         const int row = 128 * t + r;                                 // of the CTA
         const bool real = row < rows;
@@ -411,79 +463,91 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
             // (cache) which 16-token pieces of the tile are there
             uint32_t there = 0xFFu;
             if (BITS) there = __ballot_sync(0xffffffffu, lane < 8 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
-            ok = __all_sync(0xffffffffu, wait_short(sfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs));
+            ok = group_wait(2 + t, (warp & 3) == 0, sfull(t), (uint32_t)i & 1);
             if (!ok) break;
             tc_fence_after();
             const int lim = see - key0;
-            auto softmax = [&](auto masked) {
-                // -inf over the columns [c0, c0 + n) of x that the row does not see
-                auto mask = [&](uint32_t *x, int c0, int n) {
+            const bool masked = see_min < key0 + kKeys || there != 0xFFu;
+            uint64_t sum2[2] = {0, 0};
+            // 32 columns at a time, the next 32 on their way from tensor memory: their maximum, P = 2^(s - m) as FP16
+            // over columns of S that have been read.
+            auto piece = [&](uint32_t (&x)[32], uint32_t (&next)[32], int c0) {
+                tmem_wait_ld32(x);
+                if (c0 + 32 < kKeys) tmem_ld32_async(ts + c0 + 32, next);
+                if (masked) {
 #pragma unroll
-                    for (int c = 0; c < n; ++c)
-                        if (c0 + c >= lim || !((there >> ((c0 + c) >> 4)) & 1)) x[c] = 0xFF800000u;
-                };
-                // pass 1: the row's maximum.  S is read from tensor memory twice, 32 columns at a time (a read costs
-                // little, and a whole row in registers costs moves and spills)
-                float top = -INFINITY;
-#pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 64) {
-                    uint32_t x[64];
-                    tmem_ld32x2(ts + c0, ts + c0 + 32, x, x + 32);
-                    if (masked.value) mask(x, c0, 64);
-                    float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2)
-                        mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
-                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int c = 0; c < 32; ++c)
+                        if (c0 + c >= lim || !((there >> ((c0 + c) >> 4)) & 1)) x[c] = 0xFF800000u;   // -inf
                 }
-                top *= sl;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 32; c += 2)
+                    mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
                 // The maximum in use lags behind by up to 2^8: weights stay below 2^8 (FP16 holds 2^15), and O is
-                // rescaled rarely instead of in every tile.
+                // rescaled rarely.  It grows by whole numbers, so that the tile's earlier P are scaled exactly.
                 const bool grow = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float m1 = grow ? top : m;
-                    const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
+                    const float m1 = !grow ? m : m == -INFINITY ? top : m + ceilf(top - m);
+                    const float keep = m1 == m ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - m1);
                     m = m1;
                     l *= keep;
-                    if (i > 0) {
-                        // S of this step is complete, so is P V of the last one (issued before it)
+                    const uint64_t keep2 = pair(keep, keep);
+                    sum2[0] = fma2(sum2[0], keep2, 0);
+                    sum2[1] = fma2(sum2[1], keep2, 0);
+                    const __half2 hk = __float2half2_rn(keep);
+#pragma unroll 1
+                    for (int c = 0; c < c0 / 2; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(ts + c, o);
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c, o);
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-                            tmem_st32(to + c, o);
+                        for (int u = 0; u < 16; ++u) {
+                            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[u]), hk);
+                            o[u] = *reinterpret_cast<const uint32_t *>(&h);
                         }
+                        tmem_st16(ts + c, o);
+                    }
+                    // S of this step is complete, so is P V of the last one (issued before it)
+#pragma unroll 1
+                    for (int c = 0; c < (i > 0 ? D : 0); c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + c, o);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                        tmem_st16(to + c, o);
                     }
                 }
-                // pass 2: P = 2^(s - m), FP16, over the columns of S already read
                 const float sub = m == -INFINITY ? 0.0f : -m;
                 const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
-                uint64_t sum[2] = {0, 0};
+                uint32_t pk[16];
 #pragma unroll
-                for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                    uint32_t x[32], pk[16];
-                    tmem_ld32(ts + c0, x);
-                    if (masked.value) mask(x, c0, 32);
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                        float a, b;
-                        unpair(fma2(pair(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), sl2, sub2), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum[u & 1] = add2(sum[u & 1], pair(a, b));
-                        const __half2 h = __floats2half2_rn(a, b);
-                        pk[u] = *reinterpret_cast<const uint32_t *>(&h);
+                for (int u = 0; u < 16; ++u) {
+                    float e0, e1;
+                    unpair(fma2(pair(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), sl2, sub2), e0, e1);
+                    if (u % 8 < kPoly) {
+                        ex2_pair(e0, e1);
+                    } else {
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
                     }
-                    tmem_st16(ts + c0 / 2, pk);
+                    sum2[u & 1] = add2(sum2[u & 1], pair(e0, e1));
+                    const __half2 h = __floats2half2_rn(e0, e1);
+                    pk[u] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                float a, b;
-                unpair(add2(sum[0], sum[1]), a, b);
-                l += a + b;
+                tmem_st16(ts + c0 / 2, pk);
             };
-            if (see_min < key0 + kKeys || there != 0xFFu) softmax(std::true_type{});
-            else softmax(std::false_type{});
+            uint32_t x0[32], x1[32];
+            tmem_ld32_async(ts, x0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kKeys; c0 += 64) {
+                piece(x0, x1, c0);
+                piece(x1, x0, c0 + 32);
+            }
+            {
+                float e0, e1;
+                unpair(add2(sum2[0], sum2[1]), e0, e1);
+                l += e0 + e1;
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -547,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const TileArgs p
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0 && abort_flag) atomicExch(&g_tile_error, 1);
 }
 
@@ -559,8 +623,39 @@ cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // every sequence wastes at most one part of a row tile
     const int64_t tiles = (int64_t)p.T * p.G / kRows + (p.a.B < p.T ? p.a.B : p.T);
-    kernel<<<(unsigned)(tiles * p.Hkv * p.splits), kThreads, TileCfg<D>::kSmem, stream>>>(p);
+    kernel<<<(unsigned)(tiles * p.Hkv * p.splits), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
     return cudaGetLastError();
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+cudaError_t encode_rows(CUtensorMap *map, const uint16_t *x, int T, int width, int64_t ld)
+{
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dim[2] = {(cuuint64_t)width, (cuuint64_t)T}, stride[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, kKeys}, one[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t *>(x), dim, stride, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -578,8 +673,11 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream)
 {
-    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 1, 0, 0.0f, 0u};
+    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 1, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, {}, {}};
     set_scale(p, scale);
+    cudaError_t e = encode_rows(&p.map_k, k, T, Hkv * d, ldk);
+    if (e == cudaSuccess) e = encode_rows(&p.map_v, v, T, Hkv * d, ldv);
+    if (e != cudaSuccess) return e;
     return d == 128 ? launch_tile<128, 0>(p, stream) : launch_tile<64, 0>(p, stream);
 }
 
@@ -587,7 +685,7 @@ cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, in
                                const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
                                float *part, cudaStream_t stream)
 {
-    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u};
+    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u, 0x64006400u, 0x54005400u, {}, {}};
     set_scale(p, scale);
     if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream);
     return c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream);
