@@ -9,14 +9,14 @@
 // head of the group), so the heads that share a KV head share its tiles and
 // any group size fills the tile.  Two row tiles of 128 are in flight: while
 // one's softmax runs on the CUDA cores the tensor cores work for the other.
-//   warps 0-3, 4-7   softmax of row tile 0 and 1, one row per thread: S from
-//                    tensor memory, masks, maximum, exp2, P as FP16 back to
-//                    tensor memory over S; rescale O (tensor memory) when
-//                    the maximum grew by more than 2^8; at the end O to HBM.
-//   warps 8-11       loader: keys and values of the tile into a ring of
-//                    shared-memory slots in the 128-byte-swizzled layout: TMA
-//                    for FP16 rows; for a cache the codes, expanded to
-//                    fp16(s c + m) in registers (keys; warps 12-15 values).
+//   warps 0-7, 8-15  softmax of row tile 0 and 1, two threads to a row: S from
+//                    tensor memory, masks, exp2, P as FP16 back to tensor
+//                    memory over S; now and then a new maximum, and O
+//                    (tensor memory) rescaled; at the end O to HBM.
+//   loaders          keys and values of the tile into a ring of shared-memory
+//                    slots in the 128-byte-swizzled layout: a warp with TMA
+//                    for FP16 rows; for a cache two warpgroups that expand
+//                    the codes to fp16(s c + m) in registers.
 //   the last         one thread issues the MMAs: S = Q K^T (both from shared
 //                    memory), O += P V (P from tensor memory, V with its
 //                    channels contiguous).
@@ -43,14 +43,22 @@
 namespace qoq {
 namespace {
 
-// Threads: two softmax warpgroups, one loader (TMA) or two (keys, values of a cache), and the MMA issuer's.
-__host__ __device__ constexpr int tile_threads(int bits) { return bits ? 640 : 512; }
+// Threads: four softmax warpgroups; for prompts one more with the loader's and the MMA issuer's warp, for a cache two
+// loaders (keys, values) and the MMA issuer's.
+__host__ __device__ constexpr int tile_threads(int bits) { return bits ? 896 : 640; }
 constexpr int kRows = 256;          // rows of a CTA (two tiles of 128)
 constexpr int kKeys = 128;          // keys of a tile
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint64_t kBudgetNs = 2000000000ull;
 
 __device__ int g_tile_error;        // non-zero after a bounded wait ran out
+
+struct TileMisc {
+    float row[2][2][128];   // [row tile][half of the columns][row]: what the two threads of a row exchange
+    TileScan scan;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
 
 template <int D>
 struct TileCfg {
@@ -60,7 +68,9 @@ struct TileCfg {
     static constexpr int kQ = 0;                            // two Q tiles
     static constexpr int kRing = 2 * kTile;
     static constexpr int kBars = kRing + kSlots * kTile;
-    static constexpr int kSmem = kBars + 256 + 1024;        // + alignment
+    static constexpr int kMisc = kBars + 256;               // TileMisc
+    static constexpr int kSmem = kMisc + sizeof(TileMisc);  // nearly all there is: nothing else is static
+    static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 struct TileArgs {
@@ -112,9 +122,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// 2^x of two numbers below 2^7 on the FMA pipe: 2^x = 2^n 2^f with n = round(x) (adding 1.5 * 2^23 leaves n in the
+// 2^x of two numbers on the FMA pipe: 2^x = 2^n 2^f with n = round(x) (adding 1.5 * 2^23 leaves n in the
 // low bits), 2^f on [-1/2, 1/2] by the cubic of least relative error, 7.5e-5 (found by linear programming; P is
-// rounded to FP16, 4.9e-4, next).  Below 2^-126 the result is some number below 2^-125.
+// rounded to FP16, 4.9e-4, next).  Below 2^-126 the result is some number below 2^-125, from 2^7 on it is
+// nothing.
 __device__ __forceinline__ void ex2_pair(float &x, float &y)
 {
     const uint64_t t = pair(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
@@ -152,12 +163,11 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 512 with 128.
+// Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 896 with 72.
 template <int BITS>
 struct Regs {
-    static constexpr int kSoftmax = BITS ? 120 : 152, kLoader = BITS ? 88 : 72, kMma = BITS ? 64 : 80;
-    static constexpr int kLoaders = BITS ? 2 : 1;
-    static_assert(256 * kSoftmax + 128 * (kLoaders * kLoader + kMma) <= tile_threads(BITS) * (BITS ? 96 : 128), "register split");
+    static constexpr int kSoftmax = BITS ? 80 : 104, kRest = BITS ? 40 : 64;
+    static_assert(512 * kSoftmax + (BITS ? 256 * 72 : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 72 : 96), "register split");
 };
 
 // BITS 0: FP16 rows of the batch itself (prompts); 4 or 8: the cache.
@@ -165,17 +175,18 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const __grid_constant__ TileArgs p)
 {
     using C = TileCfg<D>;
-    constexpr int kThreads = tile_threads(BITS), kMmaWarp = kThreads / 32 - 4;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
-    __shared__ TileScan scan;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kThreads = tile_threads(BITS), kMmaWarp = BITS ? 24 : 17;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TileMisc &misc = *reinterpret_cast<TileMisc *>(smem + C::kMisc);
+    int &abort_flag = misc.abort_flag;
+    float (&s_row)[2][2][128] = misc.row;
+    // (the same for a warp's lanes, and the compiler is to know it)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int id = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
     const int hk = id % p.Hkv;
 
     // ---- which rows, which keys ----
-    const TileWork w = find_tile(p.a, p.T, p.G, kRows, p.few + 1, 1 << 30, id / p.Hkv, scan);
+    const TileWork w = find_tile(p.a, p.T, p.G, kRows, p.few + 1, 1 << 30, id / p.Hkv, misc.scan);
     if (w.b < 0) return;
     const int n = w.n, rows = n * p.G - w.row0;                      // rows of the sequence from this tile on
     const int first = BITS ? __ldg(p.a.kv_len + w.b) - n : 0;        // position of its new token 0
@@ -195,7 +206,6 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     for (int t = 0; t < 2; ++t) cnt[t] = max(0, min((last[t] + kKeys - 1) / kKeys, j1) - j0);
     const int steps = max(cnt[0], cnt[1]);
 
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_addr(smem);
     const uint32_t bars = sbase + C::kBars;
     auto full = [&](int s) { return bars + 8u * s; };
@@ -207,12 +217,12 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(full(s), 4);
+            mbar_init(full(s), BITS ? 4 : 1);
             mbar_init(empty(s), 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(sfull(t), 1);
-            mbar_init(pfull(t), 4);
+            mbar_init(pfull(t), 8);
             mbar_init(ofull(t), 1);
         }
         mbar_init(done, 1);
@@ -220,14 +230,14 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(smem_addr(&tmem_slot), 512);
+        tmem_alloc(smem_addr(&misc.tmem_slot), 512);
         tmem_relinquish();
     }
-    // A warpgroup's wait: one warp polls, the others sleep in a named barrier instead of polling too.
-    auto group_wait = [&](int id, bool polls, uint32_t bar, uint32_t parity) -> bool {
-        if (polls) wait_short(bar, parity, &abort_flag, kBudgetNs);
-        named_barrier(id, 128);
-        return !*(volatile int *)&abort_flag;
+    // A group's wait: one warp polls, the others sleep in a named barrier instead of polling too; it also makes the
+    // answer the same for all of them.
+    auto group_wait = [&](int id, int count, bool polls, uint32_t bar, uint32_t parity) -> bool {
+        const bool failed = polls && !wait_short(bar, parity, &abort_flag, kBudgetNs);
+        return !named_barrier_any(id, count, failed);
     };
     // ---- Q: 256 rows into shared memory, zeros past the end ----
     if (steps > 0) {
@@ -248,12 +258,14 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = misc.tmem_slot;
 
-    if (warp >= kMmaWarp) {
-        // ------------------------------------------------------------ MMA --
-        regs_down<Regs<BITS>::kMma>();
-        if (warp == kMmaWarp && lane == 0 && steps > 0) {
+    if (BITS ? warp >= 24 : warp >= 16) {
+        // ------------------------------------- MMA (and the prompts' loader) --
+        regs_down<Regs<BITS>::kRest>();
+        if (warp == kMmaWarp && steps > 0) {
+            const uint32_t lead = elect_lane();
+            auto uniform = [](bool x) { return (bool)__all_sync(0xffffffffu, x); };
             const uint32_t is = idesc_f16_m128(kKeys, false), io = idesc_f16_m128(D, true);
             const uint32_t q_lo = desc_sw128_lo(sbase + C::kQ, 1), k_lo = desc_sw128_lo(sbase + C::kRing, 1);
             const uint32_t v_lo = desc_sw128_lo(sbase + C::kRing, C::kBlock >> 4);
@@ -262,27 +274,27 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * (C::kBlock >> 4) + 2 * (kk & 3);
-                    mma_f16_ss(tmem + 128 * t, qa + off, kb + off, kDescSw128Hi, kDescSw128Hi, is, kk > 0);
+                    mma_f16_ss(lead, tmem + 128 * t, qa + off, kb + off, kDescSw128Hi, kDescSw128Hi, is, kk > 0);
                 }
-                mma_commit(sfull(t));
+                mma_commit_lead(lead, sfull(t));
             };
             auto values = [&](int t, int slot, bool accumulate) {
                 const uint32_t vb = v_lo + slot * (C::kTile >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, vb + 128 * kk, kDescSw128Hi, io,
+                    mma_f16_ts(lead, tmem + 256 + D * t, tmem + 128 * t + 8 * kk, vb + 128 * kk, kDescSw128Hi, io,
                                accumulate || kk > 0);
             };
             // ring items: K of step i is item 2i, V is item 2i + 1
             auto ready = [&](int item) {
-                return wait_short(full(item % C::kSlots), (uint32_t)(item / C::kSlots) & 1, &abort_flag, kBudgetNs);
+                return uniform(wait_short(full(item % C::kSlots), (uint32_t)(item / C::kSlots) & 1, &abort_flag, kBudgetNs));
             };
             bool ok = ready(0);
             if (ok) {
                 tc_fence_after();
                 for (int t = 0; t < 2; ++t)
                     if (cnt[t] > 0) scores(t, 0);
-                mma_commit(empty(0));
+                mma_commit_lead(lead, empty(0));
             }
             for (int i = 0; i < steps && ok; ++i) {
                 const int vi = 2 * i + 1, ki = 2 * i + 2;
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 ok = ready(vi);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (i >= cnt[t]) continue;
-                    ok = wait_short(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs);
+                    ok = uniform(wait_short(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs));
                     if (!ok) break;
                     tc_fence_after();
                     values(t, vi % C::kSlots, i > 0);
@@ -303,78 +315,69 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         }
                         scores(t, ki % C::kSlots);
                     } else {
-                        mma_commit(ofull(t));
+                        mma_commit_lead(lead, ofull(t));
                     }
                 }
                 if (!ok) break;
-                mma_commit(empty(vi % C::kSlots));
-                if (i + 1 < steps) mma_commit(empty(ki % C::kSlots));
+                mma_commit_lead(lead, empty(vi % C::kSlots));
+                if (i + 1 < steps) mma_commit_lead(lead, empty(ki % C::kSlots));
             }
             if (!ok) {      // let what was issued finish before tensor memory is freed
-                mma_commit(done);
+                mma_commit_lead(lead, done);
                 const uint64_t end = global_timer_ns() + 200000000ull;
                 while (!mbar_try_wait(done, 0) && global_timer_ns() < end) {
                 }
             }
         }
-    } else if (warp >= 8) {
-        // --------------------------------------------------------- loader --
-        regs_down<Regs<BITS>::kLoader>();
-        const int items = 2 * steps;
-        auto slot_free = [&](int item) {
-            if (item < C::kSlots) return true;
-            return (bool)__all_sync(0xffffffffu, wait_short(empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1,
-                                                            &abort_flag, kBudgetNs));
-        };
+        if (BITS == 0 && warp == 16) {
+            // TMA, except for the last values of a sequence: rows behind it are another's, or nobody's, and may hold
+            // anything, and a weight of zero does not silence an infinity.  (Keys there only make scores that are
+            // masked.)
+            const int items = 2 * steps;
+            const bool ragged = steps > 0 && (j0 + steps) * kKeys > n;
+            for (int item = 0; item < items; ++item) {
+                const int slot = item % C::kSlots;
+                if (item >= C::kSlots &&
+                    !__all_sync(0xffffffffu, wait_short(empty(slot), (uint32_t)(item / C::kSlots - 1) & 1, &abort_flag, kBudgetNs)))
+                    break;
+                const uint32_t dst = sbase + C::kRing + slot * C::kTile;
+                const int key0 = (j0 + (item >> 1)) * kKeys;
+                if (ragged && item == items - 1) {
+                    constexpr int kVecs = D / 8;
+                    for (int e = lane; e < kKeys * kVecs; e += 32) {
+                        const int row = e / kVecs, vec = e % kVecs;
+                        const bool in = key0 + row < n;
+                        cp_async16(dst + (vec >> 3) * C::kBlock + swz(row, vec),
+                                   in ? p.v + (int64_t)(t_seq + key0 + row) * p.ldv + (size_t)hk * D + vec * 8 : p.v, in);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(slot));
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(full(slot), C::kTile);
+#pragma unroll
+                    for (int blk = 0; blk < D / 64; ++blk)
+                        tma_load_2d(dst + blk * C::kBlock, item & 1 ? &p.map_v : &p.map_k, hk * D + 64 * blk, t_seq + key0,
+                                    full(slot));
+                }
+            }
+        }
+    } else if (BITS && warp >= 16) {
+        // ------------------------------------------------ loaders of a cache --
         auto signal = [&](int item) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(full(item % C::kSlots));
         };
-        if (BITS == 0) {
-            // TMA, issued by one thread, except for the last values of a sequence: rows behind it are another's, or
-            // nobody's, and may hold anything, and a weight of zero does not silence an infinity.  (Keys there only
-            // make scores that are masked.)
-            const int tid = threadIdx.x - 256;
-            const bool ragged = steps > 0 && (j0 + steps) * kKeys > n;
-            if (warp == 8) {
-                for (int item = 0; item < items - (ragged ? 1 : 0); ++item) {
-                    if (!slot_free(item)) break;
-                    if (lane == 0) {
-                        const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile, bar = full(item % C::kSlots);
-                        mbar_arrive_expect_tx(bar, C::kTile);
-                        mbar_arrive_n(bar, 3);
-#pragma unroll
-                        for (int blk = 0; blk < D / 64; ++blk)
-                            tma_load_2d(dst + blk * C::kBlock, item & 1 ? &p.map_v : &p.map_k, hk * D + 64 * blk,
-                                        t_seq + (j0 + (item >> 1)) * kKeys, bar);
-                    }
-                }
-                if (ragged) slot_free(items - 1);
-            }
-            if (ragged) {
-                named_barrier(1, 128);
-                if (!*(volatile int *)&abort_flag) {
-                    constexpr int kVecs = D / 8, kPass = 128 / kVecs;
-                    const int vec = tid % kVecs, item = items - 1, key0 = (j0 + steps - 1) * kKeys;
-                    const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile + (vec >> 3) * C::kBlock;
-                    for (int r = tid / kVecs; r < kKeys; r += kPass) {
-                        const bool in = key0 + r < n;
-                        cp_async16(dst + swz(r, vec),
-                                   in ? p.v + (int64_t)(t_seq + key0 + r) * p.ldv + (size_t)hk * D + vec * 8 : p.v, in);
-                    }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    signal(item);
-                }
-            }
-        } else {
+        {
             // One warpgroup brings the keys, the other the values.  kLanes lanes share a row's bytes, 16 each; a thread's
             // kLanes rows lie in one granule of 16 tokens, kGap apart, so one page and constant offsets serve them.
             constexpr int kB = BITS ? BITS : 4;
             constexpr int kRowBytes = D * kB / 8, kLanes = kRowBytes / 16, kGap = 16 / kLanes;
             constexpr int kVecs = 128 / kB / 8;                      // 16-byte vectors of 8 channels from 16 bytes of codes
-            const bool val = warp >= 12;
+            const bool val = warp >= 20;
             const int tid = threadIdx.x & 127, part = tid % kLanes;
             const int r0 = 16 * (tid / 16) + tid % 16 / kLanes;      // r0 % 8 is below kGap, and the other rows' r % 8 are
                                                                      // r0 % 8 ^ (kGap i % 8)
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             for (int i = 0; i < steps; ++i) {
                 const int item = 2 * i + val;
                 if (item >= C::kSlots &&
-                    !group_wait(4 + val, (warp & 3) == 0, empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1))
+                    !group_wait(6 + val, 128, (warp & 3) == 0, empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1))
                     break;
                 expand(item);
                 signal(item);
@@ -447,107 +450,108 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     } else {
         // -------------------------------------------------------- softmax --
         regs_up<Regs<BITS>::kSoftmax>();
-        const int t = warp >> 2, r = (warp & 3) * 32 + lane;         // row tile, row of it
+        // row tile, half of its columns, row of the tile (= lane of tensor memory)
+        const int t = warp >> 3, h = warp >> 2 & 1, r = (warp & 3) * 32 + lane;
+        constexpr int kCols = kKeys / 2, kOut = D / 2;               // of S and of O that are this thread's
         const int row = 128 * t + r;                                 // of the CTA
         const bool real = row < rows;
-        const int tok = real ? (w.row0 + row) / p.G : 0, g = real ? (w.row0 + row) % p.G : 0;
+        const int tok = real ? (w.row0 + row) / p.G : 0;
         const int see = real ? first + tok + 1 : 0;                  // keys 0 .. see - 1 are seen
         const int see_min = __reduce_min_sync(0xffffffffu, see);
-        const uint32_t ts = tmem + 128 * t + ((uint32_t)(warp & 3) << 21);
-        const uint32_t to = tmem + 256 + D * t + ((uint32_t)(warp & 3) << 21);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t ts = tmem + 128 * t + kCols * h + lanes;      // S; P goes over the tile's first 64 columns
+        const uint32_t tp = tmem + 128 * t + kCols / 2 * h + lanes;
+        const uint32_t to = tmem + 256 + D * t + kOut * h + lanes;
         const float sl = p.scale_log2;
-        float m = -INFINITY, l = 0.0f;                               // maximum in use (log2 units), sum
+        float m = -INFINITY, l = 0.0f;                               // maximum in use (log2 units), sum of the columns
         bool ok = true;
         for (int i = 0; i < cnt[t]; ++i) {
-            const int key0 = (j0 + i) * kKeys;
-            // (cache) which 16-token pieces of the tile are there
-            uint32_t there = 0xFFu;
-            if (BITS) there = __ballot_sync(0xffffffffu, lane < 8 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
-            ok = group_wait(2 + t, (warp & 3) == 0, sfull(t), (uint32_t)i & 1);
+            const int key0 = (j0 + i) * kKeys + kCols * h;
+            // (cache) which 16-token pieces of the columns are there
+            uint32_t there = 0xFu;
+            if (BITS) there = __ballot_sync(0xffffffffu, lane < 4 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
+            ok = group_wait(2 + t, 256, (warp & 7) == 0, sfull(t), (uint32_t)i & 1);
             if (!ok) break;
             tc_fence_after();
             const int lim = see - key0;
-            const bool masked = see_min < key0 + kKeys || there != 0xFFu;
-            uint64_t sum2[2] = {0, 0};
-            // 32 columns at a time, the next 32 on their way from tensor memory: their maximum, P = 2^(s - m) as FP16
-            // over columns of S that have been read.
-            auto piece = [&](uint32_t (&x)[32], uint32_t (&next)[32], int c0) {
-                tmem_wait_ld32(x);
-                if (c0 + 32 < kKeys) tmem_ld32_async(ts + c0 + 32, next);
-                if (masked) {
+            const bool masked = see_min < key0 + kCols || there != 0xFu;
+            // -inf over the columns [c0, c0 + 16) that the row does not see
+            auto mask = [&](uint32_t (&x)[16], int c0) {
+                const int left = (there >> (c0 / 16)) & 1 ? lim - c0 : 0;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c0 + c >= lim || !((there >> ((c0 + c) >> 4)) & 1)) x[c] = 0xFF800000u;   // -inf
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 32; c += 2)
-                    mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-                // The maximum in use lags behind by up to 2^8: weights stay below 2^8 (FP16 holds 2^15), and O is
-                // rescaled rarely.  It grows by whole numbers, so that the tile's earlier P are scaled exactly.
-                const bool grow = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float m1 = !grow ? m : m == -INFINITY ? top : m + ceilf(top - m);
-                    const float keep = m1 == m ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - m1);
-                    m = m1;
-                    l *= keep;
-                    const uint64_t keep2 = pair(keep, keep);
-                    sum2[0] = fma2(sum2[0], keep2, 0);
-                    sum2[1] = fma2(sum2[1], keep2, 0);
-                    const __half2 hk = __float2half2_rn(keep);
-#pragma unroll 1
-                    for (int c = 0; c < c0 / 2; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(ts + c, o);
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[u]), hk);
-                            o[u] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
-                        tmem_st16(ts + c, o);
-                    }
-                    // S of this step is complete, so is P V of the last one (issued before it)
-#pragma unroll 1
-                    for (int c = 0; c < (i > 0 ? D : 0); c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(to + c, o);
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-                        tmem_st16(to + c, o);
-                    }
-                }
+                for (int c = 0; c < 16; ++c)
+                    if (c >= left) x[c] = 0xFF800000u;
+            };
+            // P = 2^(s - m), FP16, with the maximum in use, 16 columns at a time, the next 16 on their way from tensor
+            // memory.  The maximum may lag far behind: as long as a thread's weights sum to at most 2^14 they fit FP16,
+            // and no maximum has to be taken.  Otherwise, and for the first keys that a row sees, the row tile's warps
+            // take it, rescale what they have and weigh the tile again.
+            uint32_t pk[kCols / 2];
+            for (int round = 0;; ++round) {
                 const float sub = m == -INFINITY ? 0.0f : -m;
                 const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
-                uint32_t pk[16];
+                uint64_t sum2[2] = {0, 0};
+                float high = -INFINITY;
+                uint32_t x[2][16];
+                tmem_ld16_async(ts, x[0]);
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    float e0, e1;
-                    unpair(fma2(pair(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), sl2, sub2), e0, e1);
-                    if (u % 8 < kPoly) {
-                        ex2_pair(e0, e1);
-                    } else {
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    uint32_t (&y)[16] = x[c0 / 16 & 1];
+                    tmem_wait_ld16(y);
+                    if (c0 + 16 < kCols) tmem_ld16_async(ts + c0 + 16, x[(c0 / 16 & 1) ^ 1]);
+                    if (masked) mask(y, c0);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(y[2 * u]), __uint_as_float(y[2 * u + 1])), sl2, sub2), e0, e1);
+                        if (u < kPoly) {
+                            high = fmaxf(fmaxf(high, e0), e1);       // (a sum would not show what is out of its range)
+                            ex2_pair(e0, e1);
+                        } else {
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                        }
+                        sum2[u & 1] = add2(sum2[u & 1], pair(e0, e1));
+                        const __half2 x2 = __floats2half2_rn(e0, e1);
+                        pk[c0 / 2 + u] = *reinterpret_cast<const uint32_t *>(&x2);
                     }
-                    sum2[u & 1] = add2(sum2[u & 1], pair(e0, e1));
-                    const __half2 h = __floats2half2_rn(e0, e1);
-                    pk[u] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                tmem_st16(ts + c0 / 2, pk);
-            };
-            uint32_t x0[32], x1[32];
-            tmem_ld32_async(ts, x0);
+                float s0, s1;
+                unpair(add2(sum2[0], sum2[1]), s0, s1);
+                s0 += s1;
+                // (also: everyone has read S before anyone writes P over it)
+                const bool again = named_barrier_any(4 + t, 256, round == 0 && (s0 > 16384.0f || high > 14.0f || (m == -INFINITY && lim > 0)));
+                if (!again) {
+                    l += s0;
+                    break;
+                }
+                float top = -INFINITY;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kKeys; c0 += 64) {
-                piece(x0, x1, c0);
-                piece(x1, x0, c0 + 32);
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    uint32_t y[16];
+                    tmem_ld16(ts + c0, y);
+                    mask(y, c0);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) top = fmaxf(top, __uint_as_float(y[c]));
+                }
+                s_row[t][h][r] = top * sl;
+                named_barrier(4 + t, 256);
+                const float m1 = fmaxf(m, fmaxf(s_row[t][0][r], s_row[t][1][r]));
+                const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
+                m = m1;
+                l *= keep;
+                // S of this step is complete, so is P V of the last one (issued before it)
+#pragma unroll 1
+                for (int c = 0; c < (i > 0 ? kOut : 0); c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(to + c, o);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                    tmem_st16(to + c, o);
+                }
+                named_barrier(4 + t, 256);       // s_row has been read
             }
-            {
-                float e0, e1;
-                unpair(add2(sum2[0], sum2[1]), e0, e1);
-                l += e0 + e1;
-            }
+            tmem_st32(tp, pk);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -555,54 +559,52 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         }
         // ---- O out ----
         if (ok && cnt[t] > 0) {
-            ok = __all_sync(0xffffffffu, wait_short(ofull(t), 0, &abort_flag, kBudgetNs));
+            ok = group_wait(2 + t, 256, (warp & 7) == 0, ofull(t), 0);
             tc_fence_after();
         }
         if (ok) {
-            const int64_t orow = (int64_t)(t_seq + tok) * p.Hq + hk * p.G + g;
+            s_row[t][h][r] = l;
+            named_barrier(4 + t, 256);
+            l = s_row[t][0][r] + s_row[t][1][r];
+            const int g = real ? (w.row0 + row) % p.G : 0;
             if (p.part == nullptr) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint16_t *dst = p.out + (int64_t)(t_seq + tok) * p.ldo + (size_t)(hk * p.G + g) * D;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(t_seq + tok) * p.ldo + (size_t)(hk * p.G + g) * D + kOut * h);
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    if (cnt[t] > 0) tmem_ld32(to + c, o);
-                    uint32_t h[16];
+                for (int c = 0; c < kOut; c += 16) {
+                    uint32_t o[16], y[8];
+                    if (cnt[t] > 0) tmem_ld16(to + c, o);
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) {
+                    for (int u = 0; u < 8; ++u) {
                         const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
-                        h[u] = l > 0.0f ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                        y[u] = l > 0.0f ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
                     }
-                    if (real) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint4 x = make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
-                            if (BITS == 4) x = from_code_order(x);
-                            reinterpret_cast<uint4 *>(dst)[c / 8 + u] = x;
-                        }
+                    for (int u = 0; u < 2; ++u) {
+                        uint4 x = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+                        if (BITS == 4) x = from_code_order(x);
+                        if (real) dst[c / 8 + u] = x;
                     }
                 }
             } else {
-                const int64_t all_rows = (int64_t)p.T * p.Hq;
-                float *dst = p.part + ((int64_t)split * all_rows + orow) * D;
-                if (real) {
+                const int64_t all_rows = (int64_t)p.T * p.Hq, orow = (int64_t)(t_seq + tok) * p.Hq + hk * p.G + g;
+                float *dst = p.part + ((int64_t)split * all_rows + orow) * D + kOut * h;
+                if (real && h == 0) {
                     float2 *ml = reinterpret_cast<float2 *>(p.part + (int64_t)p.splits * all_rows * D);
                     ml[(int64_t)split * all_rows + orow] = make_float2(m, l);
                 }
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    if (cnt[t] > 0) {
-                        tmem_ld32(to + c, o);
-                        if (real && l > 0.0f) {
+                for (int c = 0; c < (cnt[t] > 0 ? kOut : 0); c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(to + c, o);
+                    if (real && l > 0.0f) {
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const uint32_t *x = o + 8 * (u >> 1);
-                                // columns 8v .. 8v + 7 hold channels 0 4 1 5 2 6 3 7 of a 4-bit cache
-                                uint4 y = make_uint4(x[4 * (u & 1)], x[4 * (u & 1) + 1], x[4 * (u & 1) + 2], x[4 * (u & 1) + 3]);
-                                if (BITS == 4) y = make_uint4(x[u & 1], x[2 + (u & 1)], x[4 + (u & 1)], x[6 + (u & 1)]);
-                                reinterpret_cast<uint4 *>(dst)[c / 4 + u] = y;
-                            }
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t *x = o + 8 * (u >> 1);
+                            // columns 8v .. 8v + 7 hold channels 0 4 1 5 2 6 3 7 of a 4-bit cache
+                            uint4 y = make_uint4(x[4 * (u & 1)], x[4 * (u & 1) + 1], x[4 * (u & 1) + 2], x[4 * (u & 1) + 3]);
+                            if (BITS == 4) y = make_uint4(x[u & 1], x[2 + (u & 1)], x[4 + (u & 1)], x[6 + (u & 1)]);
+                            reinterpret_cast<uint4 *>(dst)[c / 4 + u] = y;
                         }
                     }
                 }
