@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     for (int u = 0; u < 8; ++u) {
                         float e0, e1;
                         unpair(fma2(pair(__uint_as_float(y[2 * u]), __uint_as_float(y[2 * u + 1])), sl2, sub2), e0, e1);
-                        if (u < kPoly) {
+                        if (BITS == 0 && u < kPoly) {
                             high = fmaxf(fmaxf(high, e0), e1);       // (a sum would not show what is out of its range)
                             ex2_pair(e0, e1);
                         } else {
@@ -617,15 +617,52 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     if (threadIdx.x == 0 && abort_flag) atomicExch(&g_tile_error, 1);
 }
 
+// Joins the splits of a cache's row tiles: a warp per (row, query head), in order.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_split_join_kernel(const float *__restrict__ part, int splits,
+                                                                          AttnBatch a, int T, int Hq, int G, int few,
+                                                                          uint16_t *__restrict__ out, int64_t ldo)
+{
+    const int64_t rows = (int64_t)T * Hq, row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31, t = (int)(row / Hq), h = (int)(row % Hq);
+    const int b = sequence_of(a.cu, a.B, t);
+    if (b < 0) return;
+    const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
+    if (t0 < 0 || t1 > T || (int64_t)(t1 - t0) * G <= few) return;       // not the tiles' (find_tile)
+    const float2 *ml = reinterpret_cast<const float2 *>(part + (int64_t)splits * rows * D) + row;
+    constexpr int kN = D / 32;
+    float M = -INFINITY, L = 0.0f, v[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+    for (int s = 0; s < splits; ++s) M = fmaxf(M, ml[s * rows].x);
+    for (int s = 0; s < splits; ++s) {
+        const float2 x = ml[s * rows];
+        if (x.y <= 0.0f) continue;                                       // saw nothing, wrote nothing
+        const float f = ex2(x.x - M);
+        L = fmaf(x.y, f, L);
+        const float *src = part + (s * rows + row) * D + kN * lane;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = fmaf(src[i], f, v[i]);
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    uint16_t *dst = out + t * ldo + (size_t)h * D + kN * lane;
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+        const __half2 x = __floats2half2_rn(v[i] * inv, v[i + 1] * inv);
+        *reinterpret_cast<__half2 *>(dst + i) = x;
+    }
+}
+
 template <int D, int BITS>
 cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
 {
     auto kernel = attn_tile_kernel<D, BITS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    // every sequence wastes at most one part of a row tile
-    const int64_t tiles = (int64_t)p.T * p.G / kRows + (p.a.B < p.T ? p.a.B : p.T);
-    kernel<<<(unsigned)(tiles * p.Hkv * p.splits), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
+    kernel<<<(unsigned)(row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * p.splits), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -671,6 +708,13 @@ void set_scale(TileArgs &p, float scale)
 
 }  // namespace
 
+int64_t row_tiles(int T, int B, int G, int few)
+{
+    // every sequence that has tiles wastes at most a part of one
+    const int64_t rows = (int64_t)T * G, most = few > 0 ? rows / (few + 1) : T;
+    return rows / kRows + (B < most ? B : most);
+}
+
 cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream)
@@ -689,8 +733,14 @@ cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, in
 {
     TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u, 0x64006400u, 0x54005400u, {}, {}};
     set_scale(p, scale);
-    if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream);
-    return c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream);
+    if (splits == 1) p.part = nullptr;
+    const cudaError_t e = d == 128 ? (c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream))
+                                   : (c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream));
+    if (e != cudaSuccess || splits == 1) return e;
+    const unsigned grid = (unsigned)(((int64_t)T * Hq + kJoinWarps - 1) / kJoinWarps);
+    auto join = d == 128 ? attn_split_join_kernel<128> : attn_split_join_kernel<64>;
+    join<<<grid, 32 * kJoinWarps, 0, stream>>>(part, splits, a, T, Hq, Hq / Hkv, few, out, ldo);
+    return cudaGetLastError();
 }
 
 cudaError_t read_and_clear_tile_error(int *value)
