@@ -8,6 +8,7 @@
 // and skips the other's sequences, so a mixed batch takes both launches and
 // no length is read on the host.  The caller's max_new saves a launch.
 #include <algorithm>
+#include <atomic>
 
 #include "qoq_attn_internal.h"
 
@@ -51,6 +52,19 @@ Plan plan(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, 
 }
 
 }  // namespace
+
+int attn_sms()
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 size_t paged_attention_workspace(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, int max_new)
 {

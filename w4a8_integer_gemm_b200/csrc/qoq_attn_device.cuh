@@ -1,5 +1,5 @@
-// qoq_attn_device.cuh -- device code the attention kernels share: which rows
-// a CTA owns, and the expansion of cached codes to FP16.
+// qoq_attn_device.cuh -- device code the attention kernels share: waits,
+// asynchronous copies, and the expansion of cached codes to FP16.
 #pragma once
 
 #include <cstdint>
@@ -54,66 +54,6 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, volati
     return true;
 }
 
-struct TileWork {
-    int b;      // sequence, -1: none
-    int row0;   // first row (new token * G + head of the group) of the tile in its sequence
-    int n;      // new tokens of the sequence
-};
-
-struct TileScan {
-    int warp[32];
-    int base, b, row0, n;
-};
-
-// Row tile number `rank` of the batch, counted from the back (the rows that
-// see most come first), over the sequences with lo <= n_b * G <= hi rows:
-// each has ceil(n_b * G / rows) tiles (a sequence with rows outside 0 .. T - 1
-// has none).  The whole CTA takes part; a thread
-// looks at one sequence per pass.
-__device__ __forceinline__ TileWork find_tile(const AttnBatch &a, int T, int G, int rows, int lo, int hi, int rank, TileScan &sc)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (threadIdx.x == 0) {
-        sc.base = 0;
-        sc.b = -1;
-    }
-    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-        const int b = a.B - 1 - (b0 + (int)threadIdx.x);
-        int n = 0, tiles = 0;
-        if (b >= 0) {
-            const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
-            n = t0 >= 0 && t1 <= T ? max(0, t1 - t0) : 0;
-            const int64_t r = (int64_t)n * G;
-            tiles = r >= lo && r <= hi ? (int)((r + rows - 1) / rows) : 0;
-        }
-        int x = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();                    // base is up to date, warp[] is free
-        if (lane == 31) sc.warp[warp] = x;
-        __syncthreads();
-        int before = sc.base, total = 0;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) before += sc.warp[w];
-            total += sc.warp[w];
-        }
-        before += x - tiles;
-        if (rank >= before && rank < before + tiles) {
-            sc.b = b;
-            sc.row0 = (tiles - 1 - (rank - before)) * rows;
-            sc.n = n;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) sc.base += total;
-        if (sc.b >= 0) break;
-    }
-    __syncthreads();
-    return {sc.b, sc.row0, sc.n};
-}
-
 // The 8 channels of a 16-byte vector in the order the 4-bit codes expand to:
 // 0 4 1 5 2 6 3 7 (the two halves of a code word give a pair).
 __device__ __forceinline__ uint4 to_code_order(uint4 v)
@@ -140,6 +80,13 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr)
+{
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+    return x;
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 x)

@@ -66,6 +66,8 @@ size_t paged_attention_workspace(int T, int B, int Hq, int Hkv, int d, int table
 cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                    const AttnBatch &a, int max_new, float scale, uint16_t *out, int64_t ldo,
                                    void *workspace, cudaStream_t stream);
+// SMs of the current device, looked up once per device.
+int attn_sms();
 // Row tiles that a batch can have at most (sequences with more than `few` rows).
 int64_t row_tiles(int T, int B, int G, int few);
 // Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows; with splits > 1 the

@@ -41,7 +41,6 @@
 // with short runs spent their time switching.)
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -759,25 +758,12 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs
     }
 }
 
-int sm_count()
-{
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    int n = cache[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 constexpr int kMaxCtas = 2 * 160;       // sizes the workspace: two CTAs per SM
 
 template <int D, int BITS, int NT>
 cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
 {
-    const int ctas = min(sm_count() * (NT == 1 ? 2 : 1), NT == 1 ? kMaxCtas : kMaxCtas / 2);
+    const int ctas = min(attn_sms() * (NT == 1 ? 2 : 1), NT == 1 ? kMaxCtas : kMaxCtas / 2);
     constexpr int smem = RowsCfg<D, BITS, NT>::kSmem;
     auto kernel = attn_rows_kernel<D, BITS, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

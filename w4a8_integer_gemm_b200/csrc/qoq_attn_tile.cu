@@ -30,6 +30,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -53,11 +54,21 @@ constexpr uint64_t kBudgetNs = 2000000000ull;
 
 __device__ int g_tile_error;        // non-zero after a bounded wait ran out
 
+constexpr int kChunks = 64;         // chunks of sequences whose first row tiles are kept at hand
 struct TileMisc {
     float row[2][2][128];   // [row tile][half of the columns][row]: what the two threads of a row exchange
-    TileScan scan;
+    int before[kChunks];    // row tiles of the sequences before each chunk
+    int total;
     uint32_t tmem_slot;
     int abort_flag;
+};
+
+// One work item: 256 rows of a sequence and KV head, and a share of its keys.
+struct TileItem {
+    int row0, rows;         // first row (new token * G + head of the group) in the sequence, rows from there on
+    int b, n, hk, split;    // sequence, its new tokens, KV head, share of the keys
+    int t_seq, first;       // first row of the sequence in the batch, position of its new token 0
+    int j0, cnt[2], steps;  // first key tile, key tiles of each row tile, of both
 };
 
 template <int D>
@@ -175,37 +186,13 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const __grid_constant__ TileArgs p)
 {
     using C = TileCfg<D>;
-    constexpr int kThreads = tile_threads(BITS), kMmaWarp = BITS ? 24 : 17;
+    constexpr int kMmaWarp = BITS ? 24 : 17, kQWarp = kMmaWarp + 1, kQWarps = BITS ? 3 : 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     TileMisc &misc = *reinterpret_cast<TileMisc *>(smem + C::kMisc);
     int &abort_flag = misc.abort_flag;
     float (&s_row)[2][2][128] = misc.row;
     // (the same for a warp's lanes, and the compiler is to know it)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int id = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-    const int hk = id % p.Hkv;
-
-    // ---- which rows, which keys ----
-    const TileWork w = find_tile(p.a, p.T, p.G, kRows, p.few + 1, 1 << 30, id / p.Hkv, misc.scan);
-    if (w.b < 0) return;
-    const int n = w.n, rows = n * p.G - w.row0;                      // rows of the sequence from this tile on
-    const int first = BITS ? __ldg(p.a.kv_len + w.b) - n : 0;        // position of its new token 0
-    const int t_seq = __ldg(p.a.cu + w.b);                           // its first row
-    // keys seen by the last row of each row tile, in key tiles
-    int last[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int r = min(rows, 128 * (t + 1)) - 1;
-        last[t] = rows > 128 * t ? max(0, first + (w.row0 + r) / p.G + 1) : 0;
-        if (BITS) last[t] = min(last[t], p.a.table_pages * p.a.page_size);
-    }
-    const int all = (max(last[0], last[1]) + kKeys - 1) / kKeys;
-    const int j0 = (int)((int64_t)all * split / p.splits), j1 = (int)((int64_t)all * (split + 1) / p.splits);
-    int cnt[2];                                                      // key tiles of each row tile here
-#pragma unroll
-    for (int t = 0; t < 2; ++t) cnt[t] = max(0, min((last[t] + kKeys - 1) / kKeys, j1) - j0);
-    const int steps = max(cnt[0], cnt[1]);
-
     const uint32_t sbase = smem_addr(smem);
     const uint32_t bars = sbase + C::kBars;
     auto full = [&](int s) { return bars + 8u * s; };
@@ -213,7 +200,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     auto sfull = [&](int t) { return bars + 8u * (2 * C::kSlots + t); };
     auto pfull = [&](int t) { return bars + 8u * (2 * C::kSlots + 2 + t); };
     auto ofull = [&](int t) { return bars + 8u * (2 * C::kSlots + 4 + t); };
-    const uint32_t done = bars + 8u * (2 * C::kSlots + 6);
+    const uint32_t qfull = bars + 8u * (2 * C::kSlots + 6), qempty = qfull + 8, done = qfull + 16;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
@@ -225,6 +212,8 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             mbar_init(pfull(t), 8);
             mbar_init(ofull(t), 1);
         }
+        mbar_init(qfull, kQWarps);
+        mbar_init(qempty, 1);
         mbar_init(done, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -239,31 +228,83 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const bool failed = polls && !wait_short(bar, parity, &abort_flag, kBudgetNs);
         return !named_barrier_any(id, count, failed);
     };
-    // ---- Q: 256 rows into shared memory, zeros past the end ----
-    if (steps > 0) {
-        for (int e = threadIdx.x; e < kRows * (D / 8); e += kThreads) {
-            const int r = e / (D / 8), vec = e % (D / 8);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int tok = (w.row0 + r) / p.G, g = (w.row0 + r) % p.G;
-                x = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(t_seq + tok) * p.ldq +
-                                                          (size_t)(hk * p.G + g) * D) + vec);
-                x = make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip);
-                if (BITS == 4) x = to_code_order(x);
-            }
-            *reinterpret_cast<uint4 *>(smem + C::kQ + (r >> 7) * C::kTile + (vec >> 3) * C::kBlock + swz(r & 127, vec)) = x;
+    // ---- the items: row tiles of all sequences, those that see most first, x KV heads x shares of the keys ----
+    // row tiles of sequence b (none if it is another kernel's, or has rows outside the batch)
+    const int per_chunk = (p.a.B + kChunks - 1) / kChunks;
+    auto tiles_of = [&](int b, int &n) -> int {
+        const int t0 = __ldg(p.a.cu + b), t1 = __ldg(p.a.cu + b + 1);
+        n = t0 >= 0 && t1 <= p.T ? max(0, t1 - t0) : 0;
+        const int64_t r = (int64_t)n * p.G;
+        return r > p.few ? (int)((r + kRows - 1) / kRows) : 0;
+    };
+    if (warp < kChunks / 32) {
+        int sum = 0, n;
+        for (int b = threadIdx.x * per_chunk; b < min(p.a.B, ((int)threadIdx.x + 1) * per_chunk); ++b) sum += tiles_of(b, n);
+        misc.before[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int x = misc.before[2 * lane], y = misc.before[2 * lane + 1];
+        int z = x + y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, z, o);
+            if (lane >= o) z += u;
         }
-        fence_proxy_async_smem();
+        misc.before[2 * lane] = z - x - y;
+        misc.before[2 * lane + 1] = z - y;
+        if (lane == 31) misc.total = z;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem_slot;
+    const int items = misc.total * p.Hkv * p.splits;
+    // Item number k of this CTA (the rounds go to and fro, since items get smaller); false: there is none.  Every role
+    // walks the same list.
+    auto get = [&](int k, TileItem &w) -> bool {
+        const int x = k * (int)gridDim.x + (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (x >= items) return false;
+        w.split = x % p.splits;
+        w.hk = x / p.splits % p.Hkv;
+        int tile = misc.total - 1 - x / p.splits / p.Hkv;
+        int lo = 0, hi = kChunks - 1;                // the last chunk that begins at or before the tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (misc.before[mid] <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        tile -= misc.before[lo];
+        for (w.b = lo * per_chunk;; ++w.b) {
+            const int c = tiles_of(w.b, w.n);
+            if (tile < c) break;
+            tile -= c;
+        }
+        w.row0 = tile * kRows;
+        w.rows = w.n * p.G - w.row0;
+        w.t_seq = __ldg(p.a.cu + w.b);
+        w.first = BITS ? max(0, __ldg(p.a.kv_len + w.b)) - w.n : 0;
+        int last[2];                                 // keys that the last row of each row tile sees, in key tiles
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int r = min(w.rows, 128 * (t + 1)) - 1;
+            last[t] = w.rows > 128 * t ? max(0, w.first + (w.row0 + r) / p.G + 1) : 0;
+            if (BITS) last[t] = min(last[t], p.a.table_pages * p.a.page_size);
+            last[t] = (last[t] + kKeys - 1) / kKeys;
+        }
+        const int all = max(last[0], last[1]), j1 = (int)((int64_t)all * (w.split + 1) / p.splits);
+        w.j0 = (int)((int64_t)all * w.split / p.splits);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) w.cnt[t] = max(0, min(last[t], j1) - w.j0);
+        w.steps = max(w.cnt[0], w.cnt[1]);
+        return true;
+    };
+    TileItem w;
 
     if (BITS ? warp >= 24 : warp >= 16) {
         // ------------------------------------- MMA (and the prompts' loader) --
         regs_down<Regs<BITS>::kRest>();
-        if (warp == kMmaWarp && steps > 0) {
+        if (warp == kMmaWarp) {
             const uint32_t lead = elect_lane();
             auto uniform = [](bool x) { return (bool)__all_sync(0xffffffffu, x); };
             const uint32_t is = idesc_f16_m128(kKeys, false), io = idesc_f16_m128(D, true);
@@ -285,42 +326,51 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     mma_f16_ts(lead, tmem + 256 + D * t, tmem + 128 * t + 8 * kk, vb + 128 * kk, kDescSw128Hi, io,
                                accumulate || kk > 0);
             };
-            // ring items: K of step i is item 2i, V is item 2i + 1
-            auto ready = [&](int item) {
-                return uniform(wait_short(full(item % C::kSlots), (uint32_t)(item / C::kSlots) & 1, &abort_flag, kBudgetNs));
+            // The ring's units go K V K V ... through all items: K of an item's step i is unit base + 2i, V the next.
+            int base = 0, slot_k = 0, done_q = 0, done_p[2] = {0, 0};        // units, their slot, uses of qfull and pfull
+            bool ok = true;
+            auto ready = [&](int unit, int slot) {
+                return uniform(wait_short(full(slot), (uint32_t)(unit / C::kSlots) & 1, &abort_flag, kBudgetNs));
             };
-            bool ok = ready(0);
-            if (ok) {
-                tc_fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (cnt[t] > 0) scores(t, 0);
-                mma_commit_lead(lead, empty(0));
-            }
-            for (int i = 0; i < steps && ok; ++i) {
-                const int vi = 2 * i + 1, ki = 2 * i + 2;
-                bool have_k = false;
-                ok = ready(vi);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (i >= cnt[t]) continue;
-                    ok = uniform(wait_short(pfull(t), (uint32_t)i & 1, &abort_flag, kBudgetNs));
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(t, vi % C::kSlots, i > 0);
-                    // S of the next step goes over P of this one: MMAs run in the order they were issued
-                    if (i + 1 < cnt[t]) {
-                        if (!have_k) {
-                            ok = have_k = ready(ki);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        scores(t, ki % C::kSlots);
-                    } else {
-                        mma_commit_lead(lead, ofull(t));
-                    }
-                }
+            auto next = [](int slot) { return slot + 1 == C::kSlots ? 0 : slot + 1; };
+            for (int k = 0; ok && get(k, w); ++k) {
+                if (w.steps == 0) continue;
+                ok = uniform(wait_short(qfull, (uint32_t)done_q++ & 1, &abort_flag, kBudgetNs)) && ready(base, slot_k);
                 if (!ok) break;
-                mma_commit_lead(lead, empty(vi % C::kSlots));
-                if (i + 1 < steps) mma_commit_lead(lead, empty(ki % C::kSlots));
+                tc_fence_after();
+                // (S goes over P of the last item: MMAs run in the order they were issued)
+                for (int t = 0; t < 2; ++t)
+                    if (w.cnt[t] > 0) scores(t, slot_k);
+                mma_commit_lead(lead, empty(slot_k));
+                if (w.steps == 1) mma_commit_lead(lead, qempty);
+                for (int i = 0; i < w.steps && ok; ++i) {
+                    const int slot_v = next(slot_k);
+                    slot_k = next(slot_v);
+                    bool have_k = false;
+                    ok = ready(base + 2 * i + 1, slot_v);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (i >= w.cnt[t]) continue;
+                        ok = uniform(wait_short(pfull(t), (uint32_t)done_p[t]++ & 1, &abort_flag, kBudgetNs));
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(t, slot_v, i > 0);
+                        if (i + 1 < w.cnt[t]) {
+                            if (!have_k) {
+                                ok = have_k = ready(base + 2 * i + 2, slot_k);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            scores(t, slot_k);
+                        } else {
+                            mma_commit_lead(lead, ofull(t));
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit_lead(lead, empty(slot_v));
+                    if (i + 1 < w.steps) mma_commit_lead(lead, empty(slot_k));
+                    if (i + 2 == w.steps) mma_commit_lead(lead, qempty);     // the item's last S was just issued
+                }
+                base += 2 * w.steps;
             }
             if (!ok) {      // let what was issued finish before tensor memory is freed
                 mma_commit_lead(lead, done);
@@ -329,48 +379,86 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
             }
         }
+        if (warp >= kQWarp && warp < kQWarp + kQWarps) {
+            // Q of the next item as soon as the last S of this one is done: 256 rows, zeros past the end
+            constexpr int kLoad = 32 * kQWarps, kVecs = D / 8;
+            const int tid = threadIdx.x - 32 * kQWarp;
+            int used = 0;
+            for (int k = 0; get(k, w); ++k) {
+                if (w.steps == 0) continue;
+                if (used > 0 && !__all_sync(0xffffffffu, wait_short(qempty, (uint32_t)(used - 1) & 1, &abort_flag, kBudgetNs))) break;
+                ++used;
+                const uint16_t *src = p.q + (int64_t)w.t_seq * p.ldq + (size_t)w.hk * p.G * D;
+                auto at = [&](int e) {
+                    const int r = e / kVecs, vec = e % kVecs;
+                    return sbase + C::kQ + (r >> 7) * C::kTile + (vec >> 3) * C::kBlock + swz(r & 127, vec);
+                };
+                for (int e = tid; e < kRows * kVecs; e += kLoad) {
+                    const int r = e / kVecs, tok = (w.row0 + r) / p.G, g = (w.row0 + r) % p.G;
+                    const bool in = r < w.rows;
+                    cp_async16(at(e), in ? src + (int64_t)tok * p.ldq + g * D + e % kVecs * 8 : p.q, in);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                if (BITS == 4 || p.flip) {                   // each thread's own vectors
+                    for (int e = tid; e < kRows * kVecs; e += kLoad) {
+                        uint4 x = ld_shared16(at(e));
+                        if (BITS == 4) x = to_code_order(x);
+                        st_shared16(at(e), make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+            }
+            cp_async_wait<0>();
+        }
         if (BITS == 0 && warp == 16) {
             // TMA, except for the last values of a sequence: rows behind it are another's, or nobody's, and may hold
             // anything, and a weight of zero does not silence an infinity.  (Keys there only make scores that are
             // masked.)
-            const int items = 2 * steps;
-            const bool ragged = steps > 0 && (j0 + steps) * kKeys > n;
-            for (int item = 0; item < items; ++item) {
-                const int slot = item % C::kSlots;
-                if (item >= C::kSlots &&
-                    !__all_sync(0xffffffffu, wait_short(empty(slot), (uint32_t)(item / C::kSlots - 1) & 1, &abort_flag, kBudgetNs)))
-                    break;
-                const uint32_t dst = sbase + C::kRing + slot * C::kTile;
-                const int key0 = (j0 + (item >> 1)) * kKeys;
-                if (ragged && item == items - 1) {
-                    constexpr int kVecs = D / 8;
-                    for (int e = lane; e < kKeys * kVecs; e += 32) {
-                        const int row = e / kVecs, vec = e % kVecs;
-                        const bool in = key0 + row < n;
-                        cp_async16(dst + (vec >> 3) * C::kBlock + swz(row, vec),
-                                   in ? p.v + (int64_t)(t_seq + key0 + row) * p.ldv + (size_t)hk * D + vec * 8 : p.v, in);
-                    }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full(slot));
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(full(slot), C::kTile);
+            int unit = 0;
+            bool ok = true;
+            for (int k = 0; ok && get(k, w); ++k) {
+                const bool ragged = w.steps > 0 && (w.j0 + w.steps) * kKeys > w.n;
+                for (int i = 0; i < 2 * w.steps; ++i, ++unit) {
+                    const int slot = unit % C::kSlots;
+                    ok = unit < C::kSlots ||
+                         __all_sync(0xffffffffu, wait_short(empty(slot), (uint32_t)(unit / C::kSlots - 1) & 1, &abort_flag, kBudgetNs));
+                    if (!ok) break;
+                    const uint32_t dst = sbase + C::kRing + slot * C::kTile;
+                    const int key0 = (w.j0 + (i >> 1)) * kKeys;
+                    if (ragged && i == 2 * w.steps - 1) {
+                        constexpr int kVecs = D / 8;
+                        for (int e = lane; e < kKeys * kVecs; e += 32) {
+                            const int row = e / kVecs, vec = e % kVecs;
+                            const bool in = key0 + row < w.n;
+                            cp_async16(dst + (vec >> 3) * C::kBlock + swz(row, vec),
+                                       in ? p.v + (int64_t)(w.t_seq + key0 + row) * p.ldv + (size_t)w.hk * D + vec * 8 : p.v, in);
+                        }
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full(slot));
+                    } else if (lane == 0) {
+                        mbar_arrive_expect_tx(full(slot), C::kTile);
 #pragma unroll
-                    for (int blk = 0; blk < D / 64; ++blk)
-                        tma_load_2d(dst + blk * C::kBlock, item & 1 ? &p.map_v : &p.map_k, hk * D + 64 * blk, t_seq + key0,
-                                    full(slot));
+                        for (int blk = 0; blk < D / 64; ++blk)
+                            tma_load_2d(dst + blk * C::kBlock, i & 1 ? &p.map_v : &p.map_k, w.hk * D + 64 * blk,
+                                        w.t_seq + key0, full(slot));
+                    }
                 }
+            }
+            if (!ok && lane == 0) {     // let the copies in flight land before the shared memory goes away
+                const uint64_t end = global_timer_ns() + 200000000ull;
+                for (int u = max(0, unit - C::kSlots); u < unit; ++u)
+                    while (!mbar_try_wait(full(u % C::kSlots), (uint32_t)(u / C::kSlots) & 1) && global_timer_ns() < end) {
+                    }
             }
         }
     } else if (BITS && warp >= 16) {
         // ------------------------------------------------ loaders of a cache --
-        auto signal = [&](int item) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full(item % C::kSlots));
-        };
         {
             // One warpgroup brings the keys, the other the values.  kLanes lanes share a row's bytes, 16 each; a thread's
             // kLanes rows lie in one granule of 16 tokens, kGap apart, so one page and constant offsets serve them.
@@ -383,18 +471,17 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                                                                      // r0 % 8 ^ (kGap i % 8)
             const uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + part * 16;
             const uint32_t *pars = reinterpret_cast<const uint32_t *>(val ? p.c.v_par : p.c.k_par);
-            const int end = first + n;
             uint4 c[kLanes];
             uint32_t pr[kLanes];
             int page = -1;                                           // of the next step to be fetched
             auto look_up = [&](int step) {
-                const int pos = (j0 + step) * kKeys + r0;
-                page = (pos & ~15) < end ? page_of(p.a, w.b, pos) : -1;
+                const int pos = (w.j0 + step) * kKeys + r0;
+                page = (pos & ~15) < w.first + w.n ? page_of(p.a, w.b, pos) : -1;
             };
             auto fetch = [&](int step) {
-                const int pos = (j0 + step) * kKeys + r0;
+                const int pos = (w.j0 + step) * kKeys + r0, end = w.first + w.n;
                 // (a pool of 2^32 rows would not fit the GPU)
-                const uint32_t row = ((uint32_t)page * p.Hkv + hk) * p.a.page_size + (pos & (p.a.page_size - 1));
+                const uint32_t row = ((uint32_t)page * p.Hkv + w.hk) * p.a.page_size + (pos & (p.a.page_size - 1));
                 const uint8_t *src = codes + (size_t)row * kRowBytes;
                 const uint32_t *par = pars + row;
 #pragma unroll
@@ -417,8 +504,8 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 const int vec = kVecs * part + (u ^ twist);
                 at[u] = (uint32_t)((vec >> 3) * C::kBlock) + swz(r0, vec);
             }
-            auto expand = [&](int item) {
-                const uint32_t dst = sbase + C::kRing + (item % C::kSlots) * C::kTile;
+            auto expand = [&](int slot) {
+                const uint32_t dst = sbase + C::kRing + slot * C::kTile;
 #pragma unroll
                 for (int i = 0; i < kLanes; ++i) {
                     const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
@@ -433,18 +520,23 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                 }
             };
-            if (steps > 0) {
+            int unit = val;
+            bool ok = true;
+            for (int k = 0; ok && get(k, w); ++k) {
+                if (w.steps == 0) continue;
                 look_up(0);
                 fetch(0);
-            }
-            for (int i = 0; i < steps; ++i) {
-                const int item = 2 * i + val;
-                if (item >= C::kSlots &&
-                    !group_wait(6 + val, 128, (warp & 3) == 0, empty(item % C::kSlots), (uint32_t)(item / C::kSlots - 1) & 1))
-                    break;
-                expand(item);
-                signal(item);
-                if (i + 1 < steps) fetch(i + 1);
+                for (int i = 0; i < w.steps; ++i, unit += 2) {
+                    const int slot = unit % C::kSlots;
+                    ok = unit < C::kSlots ||
+                         group_wait(6 + val, 128, (warp & 3) == 0, empty(slot), (uint32_t)(unit / C::kSlots - 1) & 1);
+                    if (!ok) break;
+                    expand(slot);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(slot));
+                    if (i + 1 < w.steps) fetch(i + 1);
+                }
             }
         }
     } else {
@@ -453,24 +545,26 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         // row tile, half of its columns, row of the tile (= lane of tensor memory)
         const int t = warp >> 3, h = warp >> 2 & 1, r = (warp & 3) * 32 + lane;
         constexpr int kCols = kKeys / 2, kOut = D / 2;               // of S and of O that are this thread's
-        const int row = 128 * t + r;                                 // of the CTA
-        const bool real = row < rows;
-        const int tok = real ? (w.row0 + row) / p.G : 0;
-        const int see = real ? first + tok + 1 : 0;                  // keys 0 .. see - 1 are seen
-        const int see_min = __reduce_min_sync(0xffffffffu, see);
+        const int row = 128 * t + r;                                 // of the item
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t ts = tmem + 128 * t + kCols * h + lanes;      // S; P goes over the tile's first 64 columns
         const uint32_t tp = tmem + 128 * t + kCols / 2 * h + lanes;
         const uint32_t to = tmem + 256 + D * t + kOut * h + lanes;
         const float sl = p.scale_log2;
-        float m = -INFINITY, l = 0.0f;                               // maximum in use (log2 units), sum of the columns
+        int used = 0, finished = 0;                                  // uses of sfull, of ofull
         bool ok = true;
-        for (int i = 0; i < cnt[t]; ++i) {
-            const int key0 = (j0 + i) * kKeys + kCols * h;
+        for (int k = 0; ok && get(k, w); ++k) {
+        const bool real = row < w.rows;
+        const int tok = real ? (w.row0 + row) / p.G : 0;
+        const int see = real ? w.first + tok + 1 : 0;                // keys 0 .. see - 1 are seen
+        const int see_min = __reduce_min_sync(0xffffffffu, see);
+        float m = -INFINITY, l = 0.0f;                               // maximum in use (log2 units), sum of the columns
+        for (int i = 0; i < w.cnt[t]; ++i) {
+            const int key0 = (w.j0 + i) * kKeys + kCols * h;
             // (cache) which 16-token pieces of the columns are there
             uint32_t there = 0xFu;
             if (BITS) there = __ballot_sync(0xffffffffu, lane < 4 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
-            ok = group_wait(2 + t, 256, (warp & 7) == 0, sfull(t), (uint32_t)i & 1);
+            ok = group_wait(2 + t, 256, (warp & 7) == 0, sfull(t), (uint32_t)used++ & 1);
             if (!ok) break;
             tc_fence_after();
             const int lim = see - key0;
@@ -492,13 +586,16 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
                 uint64_t sum2[2] = {0, 0};
                 float high = -INFINITY;
-                uint32_t x[2][16];
-                tmem_ld16_async(ts, x[0]);
+                // (a cache's loaders leave registers for one buffer only)
+                constexpr int kBuf = BITS ? 1 : 2;
+                uint32_t x[kBuf][16];
+                if (kBuf == 2) tmem_ld16_async(ts, x[0]);
 #pragma unroll
                 for (int c0 = 0; c0 < kCols; c0 += 16) {
-                    uint32_t (&y)[16] = x[c0 / 16 & 1];
+                    uint32_t (&y)[16] = x[c0 / 16 % kBuf];
+                    if (kBuf == 1) tmem_ld16_async(ts + c0, y);
                     tmem_wait_ld16(y);
-                    if (c0 + 16 < kCols) tmem_ld16_async(ts + c0 + 16, x[(c0 / 16 & 1) ^ 1]);
+                    if (kBuf == 2 && c0 + 16 < kCols) tmem_ld16_async(ts + c0 + 16, x[(c0 / 16 + 1) % kBuf]);
                     if (masked) mask(y, c0);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
@@ -557,23 +654,25 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             __syncwarp();
             if (lane == 0) mbar_arrive(pfull(t));
         }
+        if (!ok) break;
         // ---- O out ----
-        if (ok && cnt[t] > 0) {
-            ok = group_wait(2 + t, 256, (warp & 7) == 0, ofull(t), 0);
+        if (w.cnt[t] > 0) {
+            ok = group_wait(2 + t, 256, (warp & 7) == 0, ofull(t), (uint32_t)finished++ & 1);
+            if (!ok) break;
             tc_fence_after();
         }
-        if (ok) {
+        {
             s_row[t][h][r] = l;
             named_barrier(4 + t, 256);
             l = s_row[t][0][r] + s_row[t][1][r];
             const int g = real ? (w.row0 + row) % p.G : 0;
             if (p.part == nullptr) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(t_seq + tok) * p.ldo + (size_t)(hk * p.G + g) * D + kOut * h);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(w.t_seq + tok) * p.ldo + (size_t)(w.hk * p.G + g) * D + kOut * h);
 #pragma unroll
                 for (int c = 0; c < kOut; c += 16) {
                     uint32_t o[16], y[8];
-                    if (cnt[t] > 0) tmem_ld16(to + c, o);
+                    if (w.cnt[t] > 0) tmem_ld16(to + c, o);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
@@ -587,14 +686,14 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                 }
             } else {
-                const int64_t all_rows = (int64_t)p.T * p.Hq, orow = (int64_t)(t_seq + tok) * p.Hq + hk * p.G + g;
-                float *dst = p.part + ((int64_t)split * all_rows + orow) * D + kOut * h;
+                const int64_t all_rows = (int64_t)p.T * p.Hq, orow = (int64_t)(w.t_seq + tok) * p.Hq + w.hk * p.G + g;
+                float *dst = p.part + ((int64_t)w.split * all_rows + orow) * D + kOut * h;
                 if (real && h == 0) {
                     float2 *ml = reinterpret_cast<float2 *>(p.part + (int64_t)p.splits * all_rows * D);
-                    ml[(int64_t)split * all_rows + orow] = make_float2(m, l);
+                    ml[(int64_t)w.split * all_rows + orow] = make_float2(m, l);
                 }
 #pragma unroll
-                for (int c = 0; c < (cnt[t] > 0 ? kOut : 0); c += 16) {
+                for (int c = 0; c < (w.cnt[t] > 0 ? kOut : 0); c += 16) {
                     uint32_t o[16];
                     tmem_ld16(to + c, o);
                     if (real && l > 0.0f) {
@@ -609,6 +708,9 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                 }
             }
+        }
+        // (O has been read: the next item's first P V, which writes it, waits for this thread's next P)
+        tc_fence_before();
         }
     }
     tc_fence_before();
@@ -662,7 +764,9 @@ cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
     auto kernel = attn_tile_kernel<D, BITS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * p.splits), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
+    // one CTA per SM (shared and tensor memory allow no more), each with its share of the items
+    const int64_t items = row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * p.splits;
+    kernel<<<(unsigned)std::min<int64_t>(items, attn_sms()), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
