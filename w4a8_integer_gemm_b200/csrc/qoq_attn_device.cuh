@@ -82,6 +82,14 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 
+// 32 bytes at once, 32-byte aligned.
+__device__ __forceinline__ void st_global32(void *dst, uint4 a, uint4 b)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr)
 {
     uint4 x;

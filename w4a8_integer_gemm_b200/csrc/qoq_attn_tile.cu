@@ -54,21 +54,23 @@ constexpr uint64_t kBudgetNs = 2000000000ull;
 
 __device__ int g_tile_error;        // non-zero after a bounded wait ran out
 
+// One work item: 256 rows of a sequence and KV head, and a share of its keys.
+struct __align__(16) TileItem {
+    int row0, rows;         // first row (new token * G + head of the group) in the sequence, rows from there on
+    int b, n, hk, split;    // sequence (-1: the list is at its end), its new tokens, KV head, share of the keys
+    int t_seq, first;       // first row of the sequence in the batch, position of its new token 0
+    int j0, cnt[2], steps;  // first key tile, key tiles of each row tile, of both
+};
+
 constexpr int kChunks = 64;         // chunks of sequences whose first row tiles are kept at hand
+constexpr int kAhead = 4;           // items that the scheduler may be ahead
 struct TileMisc {
     float row[2][2][128];   // [row tile][half of the columns][row]: what the two threads of a row exchange
+    TileItem item[kAhead];
     int before[kChunks];    // row tiles of the sequences before each chunk
     int total;
     uint32_t tmem_slot;
     int abort_flag;
-};
-
-// One work item: 256 rows of a sequence and KV head, and a share of its keys.
-struct TileItem {
-    int row0, rows;         // first row (new token * G + head of the group) in the sequence, rows from there on
-    int b, n, hk, split;    // sequence, its new tokens, KV head, share of the keys
-    int t_seq, first;       // first row of the sequence in the batch, position of its new token 0
-    int j0, cnt[2], steps;  // first key tile, key tiles of each row tile, of both
 };
 
 template <int D>
@@ -96,6 +98,8 @@ struct TileArgs {
     float scale_log2;       // |scale| * log2(e)
     uint32_t flip;          // 0x80008000 when scale < 0: the sign goes into q
     uint32_t e6, e5;        // 0x64006400, 0x54005400 (expand4)
+    bool wide;              // out's rows begin on 32-byte boundaries: half as many store instructions, which the
+                            // load/store unit takes line by line
     CUtensorMap map_k, map_v;   // (prompts) [T][Hkv * D], boxes of 64 channels x 128 rows, 128-byte swizzle
 };
 
@@ -177,8 +181,8 @@ __device__ __forceinline__ void regs_down()
 // Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 896 with 72.
 template <int BITS>
 struct Regs {
-    static constexpr int kSoftmax = BITS ? 80 : 104, kRest = BITS ? 40 : 64;
-    static_assert(512 * kSoftmax + (BITS ? 256 * 72 : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 72 : 96), "register split");
+    static constexpr int kSoftmax = BITS ? 88 : 104, kLoader = BITS ? 56 : 0, kRest = BITS ? 40 : 64;
+    static_assert(512 * kSoftmax + (BITS ? 256 * kLoader : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 72 : 96), "register split");
 };
 
 // BITS 0: FP16 rows of the batch itself (prompts); 4 or 8: the cache.
@@ -186,7 +190,8 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const __grid_constant__ TileArgs p)
 {
     using C = TileCfg<D>;
-    constexpr int kMmaWarp = BITS ? 24 : 17, kQWarp = kMmaWarp + 1, kQWarps = BITS ? 3 : 2;
+    constexpr int kMmaWarp = BITS ? 24 : 17, kQWarp = kMmaWarp + 1, kQWarps = BITS ? 2 : 1;
+    constexpr int kPlanWarp = kQWarp + kQWarps, kReaders = 16 + 1 + kQWarps + (BITS ? 8 : 1);   // warps that read items
     extern __shared__ __align__(1024) uint8_t smem[];
     TileMisc &misc = *reinterpret_cast<TileMisc *>(smem + C::kMisc);
     int &abort_flag = misc.abort_flag;
@@ -201,6 +206,8 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     auto pfull = [&](int t) { return bars + 8u * (2 * C::kSlots + 2 + t); };
     auto ofull = [&](int t) { return bars + 8u * (2 * C::kSlots + 4 + t); };
     const uint32_t qfull = bars + 8u * (2 * C::kSlots + 6), qempty = qfull + 8, done = qfull + 16;
+    auto ifull = [&](int i) { return done + 8 + 8u * i; };
+    auto iempty = [&](int i) { return done + 8 + 8u * (kAhead + i); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
@@ -215,6 +222,10 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         mbar_init(qfull, kQWarps);
         mbar_init(qempty, 1);
         mbar_init(done, 1);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(ifull(i), 1);
+            mbar_init(iempty(i), kReaders);
+        }
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -259,47 +270,19 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem_slot;
-    const int items = misc.total * p.Hkv * p.splits;
-    // Item number k of this CTA (the rounds go to and fro, since items get smaller); false: there is none.  Every role
-    // walks the same list.
-    auto get = [&](int k, TileItem &w) -> bool {
-        const int x = k * (int)gridDim.x + (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if (x >= items) return false;
-        w.split = x % p.splits;
-        w.hk = x / p.splits % p.Hkv;
-        int tile = misc.total - 1 - x / p.splits / p.Hkv;
-        int lo = 0, hi = kChunks - 1;                // the last chunk that begins at or before the tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (misc.before[mid] <= tile) lo = mid;
-            else hi = mid - 1;
-        }
-        tile -= misc.before[lo];
-        for (w.b = lo * per_chunk;; ++w.b) {
-            const int c = tiles_of(w.b, w.n);
-            if (tile < c) break;
-            tile -= c;
-        }
-        w.row0 = tile * kRows;
-        w.rows = w.n * p.G - w.row0;
-        w.t_seq = __ldg(p.a.cu + w.b);
-        w.first = BITS ? max(0, __ldg(p.a.kv_len + w.b)) - w.n : 0;
-        int last[2];                                 // keys that the last row of each row tile sees, in key tiles
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int r = min(w.rows, 128 * (t + 1)) - 1;
-            last[t] = w.rows > 128 * t ? max(0, w.first + (w.row0 + r) / p.G + 1) : 0;
-            if (BITS) last[t] = min(last[t], p.a.table_pages * p.a.page_size);
-            last[t] = (last[t] + kKeys - 1) / kKeys;
-        }
-        const int all = max(last[0], last[1]), j1 = (int)((int64_t)all * (w.split + 1) / p.splits);
-        w.j0 = (int)((int64_t)all * w.split / p.splits);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) w.cnt[t] = max(0, min(last[t], j1) - w.j0);
-        w.steps = max(w.cnt[0], w.cnt[1]);
-        return true;
-    };
+    // The next item, from the scheduler's ring; false at the end of the list, or when a wait ran out.  Every role walks
+    // the same list.
+    int turn = 0;                                    // items read so far
     TileItem w;
+    auto get = [&]() -> bool {
+        const int i = turn % kAhead;
+        if (!__all_sync(0xffffffffu, wait_short(ifull(i), (uint32_t)(turn / kAhead) & 1, &abort_flag, kBudgetNs))) return false;
+        w = misc.item[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty(i));
+        ++turn;
+        return w.b >= 0;
+    };
 
     if (BITS ? warp >= 24 : warp >= 16) {
         // ------------------------------------- MMA (and the prompts' loader) --
@@ -333,7 +316,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 return uniform(wait_short(full(slot), (uint32_t)(unit / C::kSlots) & 1, &abort_flag, kBudgetNs));
             };
             auto next = [](int slot) { return slot + 1 == C::kSlots ? 0 : slot + 1; };
-            for (int k = 0; ok && get(k, w); ++k) {
+            while (ok && get()) {
                 if (w.steps == 0) continue;
                 ok = uniform(wait_short(qfull, (uint32_t)done_q++ & 1, &abort_flag, kBudgetNs)) && ready(base, slot_k);
                 if (!ok) break;
@@ -381,30 +364,47 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         }
         if (warp >= kQWarp && warp < kQWarp + kQWarps) {
             // Q of the next item as soon as the last S of this one is done: 256 rows, zeros past the end
-            constexpr int kLoad = 32 * kQWarps, kVecs = D / 8;
-            const int tid = threadIdx.x - 32 * kQWarp;
+            // Four lanes to a row, its vectors v0, v0 + 4, ...; a lane's rows are a multiple of 8 apart, so that one
+            // swizzle serves them.
+            constexpr int kPass = 8 * kQWarps, kN = D / 32;
+            const int r0 = 8 * (warp - kQWarp) + lane / 4, v0 = lane % 4;
+            const int dt = kPass / p.G, dg = kPass % p.G;    // a pass further: tokens, heads
+            uint32_t at[kN];
+#pragma unroll
+            for (int j = 0; j < kN; ++j) at[j] = sbase + C::kQ + ((v0 + 4 * j) >> 3) * C::kBlock + swz(r0, v0 + 4 * j);
             int used = 0;
-            for (int k = 0; get(k, w); ++k) {
+            while (get()) {
                 if (w.steps == 0) continue;
                 if (used > 0 && !__all_sync(0xffffffffu, wait_short(qempty, (uint32_t)(used - 1) & 1, &abort_flag, kBudgetNs))) break;
                 ++used;
-                const uint16_t *src = p.q + (int64_t)w.t_seq * p.ldq + (size_t)w.hk * p.G * D;
-                auto at = [&](int e) {
-                    const int r = e / kVecs, vec = e % kVecs;
-                    return sbase + C::kQ + (r >> 7) * C::kTile + (vec >> 3) * C::kBlock + swz(r & 127, vec);
-                };
-                for (int e = tid; e < kRows * kVecs; e += kLoad) {
-                    const int r = e / kVecs, tok = (w.row0 + r) / p.G, g = (w.row0 + r) % p.G;
+                int g = (w.row0 + r0) % p.G;
+                const uint16_t *src = p.q + (int64_t)(w.t_seq + (w.row0 + r0) / p.G) * p.ldq + (size_t)w.hk * p.G * D + 8 * v0;
+                auto offset = [](int r) { return (r >> 7) * C::kTile + (r & 127) * 128; };
+#pragma unroll 2
+                for (int r = r0; r < kRows; r += kPass) {
+                    const uint32_t off = offset(r - r0 % 8) - offset(r0 - r0 % 8);
                     const bool in = r < w.rows;
-                    cp_async16(at(e), in ? src + (int64_t)tok * p.ldq + g * D + e % kVecs * 8 : p.q, in);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) cp_async16(at[j] + off, in ? src + g * D + 32 * j : p.q, in);
+                    src += dt * p.ldq;
+                    g += dg;
+                    if (g >= p.G) {
+                        g -= p.G;
+                        src += p.ldq;
+                    }
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
-                if (BITS == 4 || p.flip) {                   // each thread's own vectors
-                    for (int e = tid; e < kRows * kVecs; e += kLoad) {
-                        uint4 x = ld_shared16(at(e));
-                        if (BITS == 4) x = to_code_order(x);
-                        st_shared16(at(e), make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip));
+                if (BITS == 4 || p.flip) {                   // each lane its own vectors
+#pragma unroll 2
+                    for (int r = r0; r < kRows; r += kPass) {
+                        const uint32_t off = offset(r - r0 % 8) - offset(r0 - r0 % 8);
+#pragma unroll
+                        for (int j = 0; j < kN; ++j) {
+                            uint4 x = ld_shared16(at[j] + off);
+                            if (BITS == 4) x = to_code_order(x);
+                            st_shared16(at[j] + off, make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip));
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -413,13 +413,66 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             }
             cp_async_wait<0>();
         }
+        if (warp == kPlanWarp) {
+            const int items = misc.total * p.Hkv * p.splits;
+            bool more = true;
+            for (int k = 0; more; ++k) {
+                // (rounds go to and fro over the CTAs, since items get smaller)
+                const int x = k * (int)gridDim.x + (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                more = x < items;
+                if (more) {
+                    w.split = x % p.splits;
+                    w.hk = x / p.splits % p.Hkv;
+                    int tile = misc.total - 1 - x / p.splits / p.Hkv;
+                    int lo = 0, hi = kChunks - 1;    // the last chunk that begins at or before the tile
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (misc.before[mid] <= tile) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    tile -= misc.before[lo];
+                    for (w.b = lo * per_chunk;; ++w.b) {
+                        const int c = tiles_of(w.b, w.n);
+                        if (tile < c) break;
+                        tile -= c;
+                    }
+                    w.row0 = tile * kRows;
+                    w.rows = w.n * p.G - w.row0;
+                    w.t_seq = __ldg(p.a.cu + w.b);
+                    w.first = BITS ? max(0, __ldg(p.a.kv_len + w.b)) - w.n : 0;
+                    int last[2];                     // keys that the last row of each row tile sees, in key tiles
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int r = min(w.rows, 128 * (t + 1)) - 1;
+                        last[t] = w.rows > 128 * t ? max(0, w.first + (w.row0 + r) / p.G + 1) : 0;
+                        if (BITS) last[t] = min(last[t], p.a.table_pages * p.a.page_size);
+                        last[t] = (last[t] + kKeys - 1) / kKeys;
+                    }
+                    const int all = max(last[0], last[1]), j1 = all * (w.split + 1) / p.splits;
+                    w.j0 = all * w.split / p.splits;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) w.cnt[t] = max(0, min(last[t], j1) - w.j0);
+                    w.steps = max(w.cnt[0], w.cnt[1]);
+                } else {
+                    w.b = -1;
+                }
+                const int i = k % kAhead;
+                if (k >= kAhead &&
+                    !__all_sync(0xffffffffu, wait_short(iempty(i), (uint32_t)(k / kAhead - 1) & 1, &abort_flag, kBudgetNs)))
+                    break;
+                if (lane == 0) {
+                    misc.item[i] = w;
+                    mbar_arrive(ifull(i));
+                }
+            }
+        }
         if (BITS == 0 && warp == 16) {
             // TMA, except for the last values of a sequence: rows behind it are another's, or nobody's, and may hold
             // anything, and a weight of zero does not silence an infinity.  (Keys there only make scores that are
             // masked.)
             int unit = 0;
             bool ok = true;
-            for (int k = 0; ok && get(k, w); ++k) {
+            while (ok && get()) {
                 const bool ragged = w.steps > 0 && (w.j0 + w.steps) * kKeys > w.n;
                 for (int i = 0; i < 2 * w.steps; ++i, ++unit) {
                     const int slot = unit % C::kSlots;
@@ -459,6 +512,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         }
     } else if (BITS && warp >= 16) {
         // ------------------------------------------------ loaders of a cache --
+        regs_down<Regs<BITS ? BITS : 4>::kLoader>();
         {
             // One warpgroup brings the keys, the other the values.  kLanes lanes share a row's bytes, 16 each; a thread's
             // kLanes rows lie in one granule of 16 tokens, kGap apart, so one page and constant offsets serve them.
@@ -471,21 +525,22 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                                                                      // r0 % 8 ^ (kGap i % 8)
             const uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + part * 16;
             const uint32_t *pars = reinterpret_cast<const uint32_t *>(val ? p.c.v_par : p.c.k_par);
-            uint4 c[kLanes];
-            uint32_t pr[kLanes];
+            constexpr int kBatch = kLanes < 4 ? kLanes : 4, kBatches = kLanes / kBatch;    // rows in registers at a time
+            uint4 c[kBatch];
+            uint32_t pr[kBatch];
             int page = -1;                                           // of the next step to be fetched
             auto look_up = [&](int step) {
                 const int pos = (w.j0 + step) * kKeys + r0;
                 page = (pos & ~15) < w.first + w.n ? page_of(p.a, w.b, pos) : -1;
             };
-            auto fetch = [&](int step) {
-                const int pos = (w.j0 + step) * kKeys + r0, end = w.first + w.n;
+            auto fetch = [&](int step, int batch) {
+                const int pos = (w.j0 + step) * kKeys + r0 + batch * kBatch * kGap, end = w.first + w.n;
                 // (a pool of 2^32 rows would not fit the GPU)
                 const uint32_t row = ((uint32_t)page * p.Hkv + w.hk) * p.a.page_size + (pos & (p.a.page_size - 1));
                 const uint8_t *src = codes + (size_t)row * kRowBytes;
                 const uint32_t *par = pars + row;
 #pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     c[i] = make_uint4(0, 0, 0, 0);
                     pr[i] = 0;
                     if (page >= 0 && pos + kGap * i < end) {         // what nobody sees becomes zeros
@@ -493,7 +548,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         pr[i] = __ldg(par + kGap * i);
                     }
                 }
-                look_up(step + 1);
+                if (batch == kBatches - 1) look_up(step + 1);
             };
             // Vector v of the thread's codes is vector kVecs * part + v of the row.  Lanes of the row's upper half store
             // theirs in another order, so that eight lanes meet eight bank groups.
@@ -504,10 +559,10 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 const int vec = kVecs * part + (u ^ twist);
                 at[u] = (uint32_t)((vec >> 3) * C::kBlock) + swz(r0, vec);
             }
-            auto expand = [&](int slot) {
-                const uint32_t dst = sbase + C::kRing + slot * C::kTile;
+            auto expand = [&](int slot, int batch) {
+                const uint32_t dst = sbase + C::kRing + slot * C::kTile + batch * kBatch * kGap * 128;
 #pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
                     for (int u = 0; u < kVecs; ++u) {
@@ -516,26 +571,32 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         if (kB == 4) x = expand4(twist ? cw[u ^ kHalf] : cw[u], pr[i], p.e6, p.e5);
                         else x = expand8(twist ? cw[2 * (u ^ kHalf) % 4] : cw[2 * u % 4],
                                          twist ? cw[(2 * (u ^ kHalf) + 1) % 4] : cw[(2 * u + 1) % 4], pr[i], p.e6);
+                        // (a batch's rows are a multiple of 8 from the first batch's: the same swizzle)
                         st_shared16(dst + (at[u] ^ ((kGap * i & 7) << 4)) + kGap * i * 128, x);
                     }
                 }
             };
+            static_assert(kBatches == 1 || kBatch * kGap % 8 == 0, "swizzle of the batches");
             int unit = val;
             bool ok = true;
-            for (int k = 0; ok && get(k, w); ++k) {
+            while (ok && get()) {
                 if (w.steps == 0) continue;
                 look_up(0);
-                fetch(0);
+                fetch(0, 0);
                 for (int i = 0; i < w.steps; ++i, unit += 2) {
                     const int slot = unit % C::kSlots;
                     ok = unit < C::kSlots ||
                          group_wait(6 + val, 128, (warp & 3) == 0, empty(slot), (uint32_t)(unit / C::kSlots - 1) & 1);
                     if (!ok) break;
-                    expand(slot);
+#pragma unroll
+                    for (int x = 0; x < kBatches; ++x) {
+                        expand(slot, x);
+                        if (x + 1 < kBatches) fetch(i, x + 1);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(slot));
-                    if (i + 1 < w.steps) fetch(i + 1);
+                    if (i + 1 < w.steps) fetch(i + 1, 0);
                 }
             }
         }
@@ -553,7 +614,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const float sl = p.scale_log2;
         int used = 0, finished = 0;                                  // uses of sfull, of ofull
         bool ok = true;
-        for (int k = 0; ok && get(k, w); ++k) {
+        while (ok && get()) {
         const bool real = row < w.rows;
         const int tok = real ? (w.row0 + row) / p.G : 0;
         const int see = real ? w.first + tok + 1 : 0;                // keys 0 .. see - 1 are seen
@@ -668,7 +729,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             const int g = real ? (w.row0 + row) % p.G : 0;
             if (p.part == nullptr) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(w.t_seq + tok) * p.ldo + (size_t)(w.hk * p.G + g) * D + kOut * h);
+                uint16_t *dst = p.out + (int64_t)(w.t_seq + tok) * p.ldo + (size_t)(w.hk * p.G + g) * D + kOut * h;
 #pragma unroll
                 for (int c = 0; c < kOut; c += 16) {
                     uint32_t o[16], y[8];
@@ -678,11 +739,18 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
                         y[u] = l > 0.0f ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
                     }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint4 x = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
-                        if (BITS == 4) x = from_code_order(x);
-                        if (real) dst[c / 8 + u] = x;
+                    uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+                    if (BITS == 4) {
+                        a = from_code_order(a);
+                        b = from_code_order(b);
+                    }
+                    if (real) {
+                        if (p.wide) {
+                            st_global32(dst + c, a, b);
+                        } else {
+                            reinterpret_cast<uint4 *>(dst + c)[0] = a;
+                            reinterpret_cast<uint4 *>(dst + c)[1] = b;
+                        }
                     }
                 }
             } else {
@@ -803,6 +871,11 @@ cudaError_t encode_rows(CUtensorMap *map, const uint16_t *x, int T, int width, i
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+bool wide_rows(const uint16_t *out, int64_t ldo)
+{
+    return (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ldo % 16 == 0;
+}
+
 void set_scale(TileArgs &p, float scale)
 {
     // a zero scale keeps a tiny one: the same uniform weights, and no 0 * infinity at masked scores
@@ -823,7 +896,7 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream)
 {
-    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 1, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, {}, {}};
+    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 1, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
     cudaError_t e = encode_rows(&p.map_k, k, T, Hkv * d, ldk);
     if (e == cudaSuccess) e = encode_rows(&p.map_v, v, T, Hkv * d, ldv);
@@ -835,7 +908,7 @@ cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, in
                                const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
                                float *part, cudaStream_t stream)
 {
-    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u, 0x64006400u, 0x54005400u, {}, {}};
+    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
     if (splits == 1) p.part = nullptr;
     const cudaError_t e = d == 128 ? (c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream))
