@@ -18,10 +18,6 @@ namespace {
 
 constexpr int kFewRows = 16;
 constexpr int kAnyRows = 1 << 30;
-#ifndef KC
-#define KC 2
-#endif
-constexpr int kCtas = KC * 148;
 
 struct Plan {
     bool rows, tiles;   // which kernels run
@@ -44,7 +40,7 @@ Plan plan(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, 
         // start and end (about as much as two key tiles) and the join
         const int64_t ctas = std::max<int64_t>(1, row_tiles(T, B, G, p.few) * Hkv);
         const int64_t keys = ((int64_t)table_pages * page_size + 127) / 128;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(kCtas + ctas - 1) / ctas, keys / 4, 16}));
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({148 / ctas, keys / 4, 16}));
     }
     p.rows_bytes = p.rows ? (rows_workspace(d) + 15) & ~(size_t)15 : 0;
     p.tiles_bytes = p.splits > 1 ? (size_t)p.splits * T * Hq * (d + 2) * sizeof(float) : 0;

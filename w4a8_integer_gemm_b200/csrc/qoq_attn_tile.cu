@@ -49,7 +49,6 @@ namespace {
 __host__ __device__ constexpr int tile_threads(int bits) { return bits ? 896 : 640; }
 constexpr int kRows = 256;          // rows of a CTA (two tiles of 128)
 constexpr int kKeys = 128;          // keys of a tile
-constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr uint64_t kBudgetNs = 2000000000ull;
 
 __device__ int g_tile_error;        // non-zero after a bounded wait ran out
@@ -67,7 +66,8 @@ constexpr int kAhead = 4;           // items that the scheduler may be ahead
 struct TileMisc {
     float row[2][2][128];   // [row tile][half of the columns][row]: what the two threads of a row exchange
     TileItem item[kAhead];
-    int before[kChunks];    // row tiles of the sequences before each chunk
+    uint8_t chunk[kChunks]; // chunks, the one with the longest sequence first
+    int before[kChunks];    // row tiles before each of them
     int total;
     uint32_t tmem_slot;
     int abort_flag;
@@ -81,7 +81,7 @@ struct TileCfg {
     static constexpr int kQ = 0;                            // two Q tiles
     static constexpr int kRing = 2 * kTile;
     static constexpr int kBars = kRing + kSlots * kTile;
-    static constexpr int kMisc = kBars + 256;               // TileMisc
+    static constexpr int kMisc = kBars + (((2 * kSlots + 9 + 2 * kAhead) * 8 + 15) & ~15);   // barriers, TileMisc
     static constexpr int kSmem = kMisc + sizeof(TileMisc);  // nearly all there is: nothing else is static
     static_assert(kSmem <= 232448, "shared memory of a block");
 };
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const bool failed = polls && !wait_short(bar, parity, &abort_flag, kBudgetNs);
         return !named_barrier_any(id, count, failed);
     };
-    // ---- the items: row tiles of all sequences, those that see most first, x KV heads x shares of the keys ----
+    // ---- the items: row tiles of all sequences x KV heads x shares of the keys, those that see most first ----
     // row tiles of sequence b (none if it is another kernel's, or has rows outside the batch)
     const int per_chunk = (p.a.B + kChunks - 1) / kChunks;
     auto tiles_of = [&](int b, int &n) -> int {
@@ -249,9 +249,21 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         return r > p.few ? (int)((r + kRows - 1) / kRows) : 0;
     };
     if (warp < kChunks / 32) {
-        int sum = 0, n;
-        for (int b = threadIdx.x * per_chunk; b < min(p.a.B, ((int)threadIdx.x + 1) * per_chunk); ++b) sum += tiles_of(b, n);
-        misc.before[threadIdx.x] = sum;
+        int *length = reinterpret_cast<int *>(misc.row);
+        int sum = 0, n, len = 0;
+        for (int b = threadIdx.x * per_chunk; b < min(p.a.B, ((int)threadIdx.x + 1) * per_chunk); ++b) {
+            sum += tiles_of(b, n);
+            len = max(len, BITS ? __ldg(p.a.kv_len + b) : n);
+        }
+        length[threadIdx.x] = sum > 0 ? len : -1;
+        named_barrier(1, kChunks);
+        int rank = 0;                                // chunks by their longest sequence
+        for (int j = 0; j < kChunks; ++j) {
+            const int x = length[j], y = length[threadIdx.x];
+            rank += x > y || (x == y && j < (int)threadIdx.x);
+        }
+        misc.chunk[rank] = threadIdx.x;
+        misc.before[rank] = sum;
     }
     __syncthreads();
     if (warp == 0) {
@@ -423,7 +435,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 if (more) {
                     w.split = x % p.splits;
                     w.hk = x / p.splits % p.Hkv;
-                    int tile = misc.total - 1 - x / p.splits / p.Hkv;
+                    int tile = x / p.splits / p.Hkv, count;
                     int lo = 0, hi = kChunks - 1;    // the last chunk that begins at or before the tile
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) >> 1;
@@ -431,12 +443,12 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         else hi = mid - 1;
                     }
                     tile -= misc.before[lo];
-                    for (w.b = lo * per_chunk;; ++w.b) {
-                        const int c = tiles_of(w.b, w.n);
-                        if (tile < c) break;
-                        tile -= c;
+                    for (w.b = misc.chunk[lo] * per_chunk;; ++w.b) {
+                        count = tiles_of(w.b, w.n);
+                        if (tile < count) break;
+                        tile -= count;
                     }
-                    w.row0 = tile * kRows;
+                    w.row0 = (count - 1 - tile) * kRows;
                     w.rows = w.n * p.G - w.row0;
                     w.t_seq = __ldg(p.a.cu + w.b);
                     w.first = BITS ? max(0, __ldg(p.a.kv_len + w.b)) - w.n : 0;
