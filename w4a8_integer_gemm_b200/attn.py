@@ -18,7 +18,6 @@ page).  All of it stays on the device, so the calls can be captured.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -45,49 +44,69 @@ ATTN_SIGNATURES = {
 }
 
 
-def _fn(name):
-    from . import lib
-    return getattr(lib(), name)
+_FN = {}    # the library's functions by name, looked up once
+
+# What torch.cuda.current_stream() and current_device() return, without building objects: a decode step's calls are
+# a few microseconds of GPU work each, and the two cost as much.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _check(name: str, status: int):
+def _call(name: str, *args):
+    f = _FN.get(name)
+    if f is None:
+        from . import lib
+        f = _FN[name] = getattr(lib(), name)
+    status = f(*args)
     if status != 0:
         from . import QoQError
         raise QoQError(name, status)
 
 
-def _on(stream, device):
-    """(raw stream, context in which outputs and scratch are allocated): memory is taken from the pool of the
-    stream that uses it."""
+def _stream(stream, device: int):
+    """The raw stream to launch on."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, contextlib.nullcontext()
+        return _raw_stream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _empty(stream, device: int, shape, dtype=torch.float16):
+    """Memory from the pool of the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _heads(x: torch.Tensor, name: str, device=None, heads=None, d=None, rows=None):
-    """x fp16 [T, H, d] on the current device, the heads of a row next to one another; any row stride that is a
-    multiple of 8."""
-    if not x.is_cuda or x.dtype != torch.float16 or x.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA float16 tensor [T, H, d]")
+def _device(x: torch.Tensor, name: str) -> int:
+    """The index of x's device, which has to be the current one."""
+    i = x.get_device()
+    if i < 0 or i != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return i
+
+
+def _heads(x: torch.Tensor, name: str, device: int, heads=None, d=None, rows=None):
+    """(address, row stride) of x fp16 [T, H, d], the heads of a row next to one another."""
+    if x.dtype is not torch.float16 or x.dim() != 3 or x.get_device() != device:
+        raise ValueError(f"{name} must be a float16 tensor [T, H, d] on the current CUDA device")
     T, H, D = x.shape
-    if T > 0 and (x.stride(2) != 1 or (H > 1 and x.stride(1) != D)):
-        raise ValueError(f"{name}: each row's heads must be contiguous")
-    if device is None:
-        if x.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{name} is on another device than the current one")
-    elif x.device != device:
-        raise ValueError(f"{name} is on another device")
     if (heads is not None and H != heads) or (d is not None and D != d) or (rows is not None and T != rows):
         raise ValueError(f"{name} has shape {tuple(x.shape)}")
-    return x.data_ptr(), (x.stride(0) if T > 1 else H * D)
+    s = x.stride()
+    if T > 0 and (s[2] != 1 or (H > 1 and s[1] != D)):
+        raise ValueError(f"{name}: each row's heads must be contiguous")
+    return x.data_ptr(), s[0] if T > 1 else H * D
 
 
-def _index(x: torch.Tensor, name: str, shape, device):
-    if not x.is_cuda or x.dtype != torch.int32 or not x.is_contiguous() or x.device != device:
+def _index(x: torch.Tensor, name: str, device: int, n=None):
+    """The address of a contiguous int32 array [n]."""
+    if x.dtype is not torch.int32 or x.get_device() != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on the rows' device")
-    if x.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, x.shape)):
+    if x.dim() != 1 or (n is not None and x.shape[0] != n):
         raise ValueError(f"{name} has shape {tuple(x.shape)}")
     return x.data_ptr()
 
@@ -101,9 +120,9 @@ class Rotary:
     interleaved: bool = False
     amplitude: float = 1.0
 
-    def args(self, device):
+    def args(self, device: int):
         f = self.freq
-        if not f.is_cuda or f.dtype != torch.float64 or f.dim() != 1 or not f.is_contiguous() or f.device != device:
+        if f.dtype is not torch.float64 or f.dim() != 1 or f.get_device() != device or not f.is_contiguous():
             raise ValueError("freq must be a contiguous float64 tensor [rot / 2] on the rows' device")
         return f.data_ptr(), 2 * f.numel(), int(bool(self.interleaved)), float(self.amplitude)
 
@@ -151,21 +170,20 @@ def qattn_rotary(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: 
                  stream=None) -> torch.Tensor:
     """x fp16 [T, H, d] with the first 2 * len(freq) channels of each head turned by positions int32 [T]; out may be
     x."""
-    px, ldx = _heads(x, "x")
+    dev = _device(x, "x")
+    px, ldx = _heads(x, "x", dev)
     T, H, d = x.shape
-    pp = _index(positions, "positions", (T,), x.device)
-    freq, rot, inter, amp = rotary.args(x.device)
-    s, alloc = _on(stream, x.device)
+    pp = _index(positions, "positions", dev, T)
+    freq, rot, inter, amp = rotary.args(dev)
     if out is None:
-        with alloc:
-            out = torch.empty(T, H, d, dtype=torch.float16, device=x.device)
-    po, ldo = _heads(out, "out", x.device, H, d, T)
-    _check("qattn_rotary", _fn("qattn_rotary")(px, ldx, pp, freq, T, H, d, rot, inter, amp, po, ldo, s))
+        out = _empty(stream, dev, (T, H, d))
+    po, ldo = _heads(out, "out", dev, H, d, T)
+    _call("qattn_rotary", px, ldx, pp, freq, T, H, d, rot, inter, amp, po, ldo, _stream(stream, dev))
     return out
 
 
 # ----------------------------------------------------------------- cache ----
-@dataclass
+@dataclass(frozen=True)
 class PagedKVCache:
     """A pool of pages of 4- or 8-bit keys and values (layouts of include/qoq_attn.h)."""
     k_codes: torch.Tensor   # uint8 [pages, Hkv, page_size, d * bits / 8]
@@ -173,6 +191,22 @@ class PagedKVCache:
     k_par: torch.Tensor     # fp16 [pages, Hkv, page_size, 2]: scale, minimum
     v_par: torch.Tensor
     bits: int               # 4 or 8
+
+    def __post_init__(self):
+        if self.bits not in (4, 8):
+            raise ValueError("a cache has 4 or 8 bits")
+        kc, vc, kp, vp = self.k_codes, self.v_codes, self.k_par, self.v_par
+        n, dev = kc.shape, kc.get_device()
+        if len(n) != 4 or vc.shape != n or kp.shape != (n[0], n[1], n[2], 2) or vp.shape != kp.shape:
+            raise ValueError("the cache's arrays do not fit one another")
+        if kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 or kp.dtype is not torch.float16 or \
+                vp.dtype is not torch.float16:
+            raise ValueError("a cache has uint8 codes and float16 parameters")
+        for t in (kc, vc, kp, vp):
+            if t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("the cache's arrays must be contiguous, on one device")
+        object.__setattr__(self, "_args", (dev, (kc.data_ptr(), vc.data_ptr(), kp.data_ptr(), vp.data_ptr(), self.bits, n[2],
+                                                 n[0], n[1], n[3] * 8 // self.bits)))
 
     @property
     def pages(self) -> int:
@@ -186,19 +220,12 @@ class PagedKVCache:
     def d(self) -> int:
         return self.k_codes.shape[3] * 8 // self.bits
 
-    def args(self, device):
-        """(k_codes, v_codes, k_par, v_par, bits, page_size, pages, Hkv, d), checked."""
-        if self.bits not in (4, 8):
-            raise ValueError("a cache has 4 or 8 bits")
-        n = self.k_codes.shape
-        for t, name, dtype in ((self.k_codes, "k_codes", torch.uint8), (self.v_codes, "v_codes", torch.uint8),
-                               (self.k_par, "k_par", torch.float16), (self.v_par, "v_par", torch.float16)):
-            if t.dtype != dtype or t.device != device or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor on the rows' device")
-            if len(n) != 4 or t.shape != (n if dtype == torch.uint8 else n[:3] + (2,)):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}")
-        return (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_par.data_ptr(), self.v_par.data_ptr(),
-                self.bits, n[2], n[0], n[1], n[3] * 8 // self.bits)
+    def args(self, device: int):
+        """(k_codes, v_codes, k_par, v_par, bits, page_size, pages, Hkv, d)"""
+        dev, args = self._args
+        if dev != device:
+            raise ValueError("the cache is on another device than the rows")
+        return args
 
 
 def paged_kv_cache(pages: int, Hkv: int, d: int, bits: int = 4, page_size: int = 64, device="cuda") -> PagedKVCache:
@@ -210,13 +237,12 @@ def paged_kv_cache(pages: int, Hkv: int, d: int, bits: int = 4, page_size: int =
     return PagedKVCache(*codes, *par, bits)
 
 
-def _batch(table, cu, kv_len, device):
+def _batch(table, cu, kv_len, device: int):
     """(table, table_pages, cu, kv_len, B), checked."""
-    if table.dim() != 2:
-        raise ValueError("table must be [B, pages per sequence]")
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != device or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 tensor [B, pages per sequence] on the rows' device")
     B, P = table.shape
-    return (_index(table, "table", (B, P), device), P, _index(cu, "cu", (B + 1,), device),
-            _index(kv_len, "kv_len", (B,), device), B)
+    return table.data_ptr(), P, _index(cu, "cu", device, B + 1), _index(kv_len, "kv_len", device, B), B
 
 
 def qattn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, table: torch.Tensor, cu: torch.Tensor,
@@ -225,30 +251,27 @@ def qattn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, ta
     """Quantises the new tokens' k and v fp16 [T, Hkv, d] into their pages.  With `rotary` the keys are turned by
     their positions first; with `rotary` and q fp16 [T, Hq, d], returns q turned by them (in q_out, which may be
     q).  Rows of no sequence are left alone, in the cache and in q_out."""
-    pk, ldk = _heads(k, "k")
+    dev = _device(k, "k")
+    pk, ldk = _heads(k, "k", dev)
     T, Hkv, d = k.shape
-    dev = k.device
     pv, ldv = _heads(v, "v", dev, Hkv, d, T)
     kc, vc, kp, vp, bits, page, pages, ch, cd = cache.args(dev)
-    if (ch, cd) != (Hkv, d):
+    if ch != Hkv or cd != d:
         raise ValueError("the cache's heads differ from those of k")
-    if q is not None and rotary is None:
-        raise ValueError("q is only rotated: it needs `rotary`")
     freq, rot, inter, amp = rotary.args(dev) if rotary is not None else (None, 0, 0, 1.0)
-    b = _batch(table, cu, kv_len, dev)
-    s, alloc = _on(stream, dev)
-    pq = ldq = po = ldo = None
-    Hq = 0
+    tab, P, pc, pl, B = _batch(table, cu, kv_len, dev)
+    pq = po = None
+    ldq = ldo = Hq = 0
     if q is not None:
+        if rotary is None:
+            raise ValueError("q is only rotated: it needs `rotary`")
         pq, ldq = _heads(q, "q", dev, None, d, T)
         Hq = q.shape[1]
         if q_out is None:
-            with alloc:
-                q_out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
+            q_out = _empty(stream, dev, (T, Hq, d))
         po, ldo = _heads(q_out, "q_out", dev, Hq, d, T)
-    _check("qattn_cache_append",
-           _fn("qattn_cache_append")(pk, ldk, pv, ldv, pq, ldq or 0, po, ldo or 0, T, Hq, Hkv, d, freq, rot, inter, amp,
-                                     bits, page, pages, kc, vc, kp, vp, *b[:4], b[4], s))
+    _call("qattn_cache_append", pk, ldk, pv, ldv, pq, ldq, po, ldo, T, Hq, Hkv, d, freq, rot, inter, amp, bits, page,
+          pages, kc, vc, kp, vp, tab, P, pc, pl, B, _stream(stream, dev))
     return q_out if q is not None else None
 
 
@@ -256,28 +279,27 @@ def qattn_cache_read(cache: PagedKVCache, table: torch.Tensor, cu: torch.Tensor,
                      K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None, stream=None):
     """(K, V) fp16 [total, Hkv, d]: the last cu[b+1] - cu[b] cached tokens of each sequence, as the values their codes
     stand for (zeros where a page is absent)."""
-    dev = cache.k_codes.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("the cache is on another device than the current one")
+    dev = _device(cache.k_codes, "the cache")
     kc, vc, kp, vp, bits, page, pages, Hkv, d = cache.args(dev)
-    b = _batch(table, cu, kv_len, dev)
-    s, alloc = _on(stream, dev)
-    with alloc:
-        K = torch.empty(total, Hkv, d, dtype=torch.float16, device=dev) if K is None else K
-        V = torch.empty(total, Hkv, d, dtype=torch.float16, device=dev) if V is None else V
-    for x, name in ((K, "K"), (V, "V")):
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        _heads(x, name, dev, Hkv, d, total)
-    _check("qattn_cache_read", _fn("qattn_cache_read")(kc, vc, kp, vp, bits, page, pages, Hkv, d, *b[:4], b[4], total,
-                                                       K.data_ptr(), V.data_ptr(), s))
+    tab, P, pc, pl, B = _batch(table, cu, kv_len, dev)
+    if K is None:
+        K = _empty(stream, dev, (total, Hkv, d))
+    if V is None:
+        V = _empty(stream, dev, (total, Hkv, d))
+    pk, lk = _heads(K, "K", dev, Hkv, d, total)
+    pv, lv = _heads(V, "V", dev, Hkv, d, total)
+    if lk != Hkv * d or lv != Hkv * d:
+        raise ValueError("K and V must be contiguous")
+    _call("qattn_cache_read", kc, vc, kp, vp, bits, page, pages, Hkv, d, tab, P, pc, pl, B, total, pk, pv,
+          _stream(stream, dev))
     return K, V
 
 
 # ------------------------------------------------------------- attention ----
 def qattn_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, d: int, table_pages: int, page_size: int,
                                           max_new: int) -> int:
-    return int(_fn("qattn_paged_attention_workspace_bytes")(T, B, Hq, Hkv, d, table_pages, page_size, max_new))
+    from . import lib
+    return int(lib().qattn_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, table_pages, page_size, max_new))
 
 
 def qattn_paged_attention(q: torch.Tensor, cache: PagedKVCache, table: torch.Tensor, cu: torch.Tensor,
@@ -287,28 +309,25 @@ def qattn_paged_attention(q: torch.Tensor, cache: PagedKVCache, table: torch.Ten
     """Attention of the new tokens' q fp16 [T, Hq, d] over the cache, which holds their keys and values already:
     each sees the cached tokens up to its own position.  `max_new`: an upper bound of the sequences' new tokens
     where the caller has one (1 for a decode step); it only picks kernels.  `scale` defaults to 1 / sqrt(d)."""
-    pq, ldq = _heads(q, "q")
+    dev = _device(q, "q")
+    pq, ldq = _heads(q, "q", dev)
     T, Hq, d = q.shape
-    dev = q.device
     kc, vc, kp, vp, bits, page, pages, Hkv, cd = cache.args(dev)
     if cd != d:
         raise ValueError("the cache's head dimension differs from that of q")
-    b = _batch(table, cu, kv_len, dev)
+    tab, P, pc, pl, B = _batch(table, cu, kv_len, dev)
     most = max(1, T if max_new is None else int(max_new))
-    s, alloc = _on(stream, dev)
-    with alloc:
-        if out is None:
-            out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
-        if workspace is None:
-            need = qattn_paged_attention_workspace_bytes(T, b[4], Hq, Hkv, d, b[1], page, most)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if out is None:
+        out = _empty(stream, dev, (T, Hq, d))
     po, ldo = _heads(out, "out", dev, Hq, d, T)
-    if workspace.device != dev or not workspace.is_contiguous():
+    if workspace is None:
+        need = qattn_paged_attention_workspace_bytes(T, B, Hq, Hkv, d, P, page, most)
+        workspace = _empty(stream, dev, (max(need, 16),), torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the rows' device")
-    _check("qattn_paged_attention",
-           _fn("qattn_paged_attention")(pq, ldq, T, Hq, Hkv, d, kc, vc, kp, vp, bits, page, pages, *b[:4], b[4], most,
-                                        d ** -0.5 if scale is None else float(scale), po, ldo, workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), s))
+    _call("qattn_paged_attention", pq, ldq, T, Hq, Hkv, d, kc, vc, kp, vp, bits, page, pages, tab, P, pc, pl, B, most,
+          d ** -0.5 if scale is None else float(scale), po, ldo, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _stream(stream, dev))
     return out
 
 
@@ -317,19 +336,16 @@ def qattn_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu
                            stream=None) -> torch.Tensor:
     """Causal attention within each packed prompt: q fp16 [T, Hq, d], k and v fp16 [T, Hkv, d], cu int32 [B + 1] ->
     fp16 [T, Hq, d].  `scale` defaults to 1 / sqrt(d)."""
-    pq, ldq = _heads(q, "q")
+    dev = _device(q, "q")
+    pq, ldq = _heads(q, "q", dev)
     T, Hq, d = q.shape
-    dev = q.device
     pk, ldk = _heads(k, "k", dev, None, d, T)
     Hkv = k.shape[1]
     pv, ldv = _heads(v, "v", dev, Hkv, d, T)
-    pc = _index(cu, "cu", (None,), dev)
-    s, alloc = _on(stream, dev)
+    pc = _index(cu, "cu", dev)
     if out is None:
-        with alloc:
-            out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
+        out = _empty(stream, dev, (T, Hq, d))
     po, ldo = _heads(out, "out", dev, Hq, d, T)
-    _check("qattn_prompt_attention",
-           _fn("qattn_prompt_attention")(pq, ldq, pk, ldk, pv, ldv, T, Hq, Hkv, d, pc, cu.numel() - 1,
-                                         d ** -0.5 if scale is None else float(scale), po, ldo, s))
+    _call("qattn_prompt_attention", pq, ldq, pk, ldk, pv, ldv, T, Hq, Hkv, d, pc, cu.shape[0] - 1,
+          d ** -0.5 if scale is None else float(scale), po, ldo, _stream(stream, dev))
     return out
