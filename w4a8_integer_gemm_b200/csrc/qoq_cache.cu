@@ -23,6 +23,7 @@
 // the IEEE division only next to a rounding boundary.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "qoq_attn_device.cuh"
@@ -34,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 4;          // tokens per CTA
+constexpr int kMaxReadTok = 16;     // the same for the reader
 
 // (amplitude * cos, amplitude * sin) of position pos at frequency f.
 __device__ __forceinline__ double2 turn(int pos, double f, float amplitude)
@@ -154,11 +156,17 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const uint16_t *__rest
     for (int i = threadIdx.x >> 6; i < n; i += kThreads >> 6)
         make_turns(fast + i * pairs, exact + i * pairs, __ldg(pos + t0 + i), r, threadIdx.x & 63, 64);
     __syncthreads();
-    const int slots = d / 16;
+    // A thread's slot stays the same, its head advances (without a division); threads past a multiple of the slots idle.
+    const int slots = d / 16, rows = kThreads / slots, j = threadIdx.x % slots;
+    if ((int)threadIdx.x >= rows * slots) return;
     const float bound = turn_bound(r.amplitude);
-    for (int e = threadIdx.x; e < n * H * slots; e += kThreads) {
-        const int j = e % slots, h = e / slots % H, i = e / (slots * H);
-        const int2 at = slot_vectors(j, r.rot, INTER);
+    const int2 at = slot_vectors(j, r.rot, INTER);
+    for (int h = threadIdx.x / slots, i = 0;; h += rows) {
+        while (h >= H) {
+            h -= H;
+            ++i;
+        }
+        if (i >= n) break;
         const uint4 *src = reinterpret_cast<const uint4 *>(x + (t0 + i) * ldx + (size_t)h * d);
         uint4 *dst = reinterpret_cast<uint4 *>(y + (t0 + i) * ldy + (size_t)h * d);
         uint4 va = src[at.x], vb = src[at.y];
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(AttnCache c, AttnB
                                                               uint16_t *__restrict__ V)
 {
     constexpr int kVecs = D / 8, kAhead = 4;
-    __shared__ int s_off[kMaxTok], s_page[kMaxTok];
+    __shared__ int s_off[kMaxReadTok], s_page[kMaxReadTok];
     const int t0 = blockIdx.x * tb, n = min(tb, T - t0);
     if (threadIdx.x < n) {
         const int t = t0 + threadIdx.x, b = sequence_of(a.cu, a.B, t);
@@ -312,33 +320,41 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(AttnCache c, AttnB
         s_off[threadIdx.x] = pos & (a.page_size - 1);
     }
     __syncthreads();
-    // items of a token: (head, key or value, vector); a thread's vector is always the same
-    const int items = n * Hkv * 2 * kVecs, j = threadIdx.x % kVecs;
-    for (int e0 = threadIdx.x; e0 < items; e0 += kAhead * kThreads) {
+    // rows of a token: (head, key or value); a thread's vector stays the same, its row advances by constants
+    const int rows = 2 * Hkv, j = threadIdx.x % kVecs;
+    constexpr int kStep = kThreads / kVecs;
+    const int di = kStep / rows, dx = kStep % rows;
+    int i = (int)threadIdx.x / kVecs / rows, x = (int)threadIdx.x / kVecs % rows;
+    while (i < n) {
         uint32_t par[kAhead];
         uint2 codes[kAhead];
+        uint4 *dst[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int x = (e0 + u * kThreads) / kVecs, h = x / 2 % Hkv, i = x / (2 * Hkv);
-            const int page = i < n ? s_page[i] : -1;
+            const int page = i < n ? s_page[i] : -2;
             par[u] = 0;
             codes[u] = make_uint2(0, 0);
+            dst[u] = page == -2 ? nullptr
+                                : reinterpret_cast<uint4 *>((x & 1 ? V : K) + ((size_t)(t0 + i) * Hkv + (x >> 1)) * D) + j;
             if (page >= 0) {
-                const size_t row = ((size_t)page * Hkv + h) * a.page_size + s_off[i];
+                const size_t row = ((size_t)page * Hkv + (x >> 1)) * a.page_size + s_off[i];
                 const uint8_t *src = (x & 1 ? c.v_codes : c.k_codes) + row * (D * BITS / 8);
                 par[u] = __ldg(reinterpret_cast<const uint32_t *>(x & 1 ? c.v_par : c.k_par) + row);
                 if (BITS == 4) codes[u].x = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
                 else codes[u] = __ldg(reinterpret_cast<const uint2 *>(src) + j);
             }
+            i += di;
+            x += dx;
+            if (x >= rows) {
+                x -= rows;
+                ++i;
+            }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int x = (e0 + u * kThreads) / kVecs, h = x / 2 % Hkv, i = x / (2 * Hkv);
-            if (i >= n || s_page[i] == -2) continue;
             // (an absent page: codes and parameters 0, so zeros)
-            const uint4 o = BITS == 4 ? from_code_order(expand4(codes[u].x, par[u], e6, e5))
-                                      : expand8(codes[u].x, codes[u].y, par[u], e6);
-            reinterpret_cast<uint4 *>((x & 1 ? V : K) + ((size_t)(t0 + i) * Hkv + h) * D)[j] = o;
+            if (dst[u]) *dst[u] = BITS == 4 ? from_code_order(expand4(codes[u].x, par[u], e6, e5))
+                                            : expand8(codes[u].x, codes[u].y, par[u], e6);
         }
     }
 }
@@ -379,7 +395,9 @@ cudaError_t launch_cache_append(const uint16_t *k, int64_t ldk, const uint16_t *
 cudaError_t launch_cache_read(const AttnCache &c, const AttnBatch &a, int T, int Hkv, int d, uint16_t *K, uint16_t *V,
                               cudaStream_t stream)
 {
-    const int tb = tokens_per_cta(T);
+    // eight vectors per thread, as long as that leaves four CTAs per SM
+    const int want = 8 * kThreads / (2 * Hkv * (d / 8)), most = T / (4 * 148);
+    const int tb = std::max(1, std::min({want, most, kMaxReadTok}));
     auto run = [&](auto kernel) { kernel<<<(T + tb - 1) / tb, kThreads, 0, stream>>>(c, a, T, Hkv, tb, 0x64006400u, 0x54005400u, K, V); };
     if (d == 128) c.bits == 4 ? run(cache_read_kernel<128, 4>) : run(cache_read_kernel<128, 8>);
     else c.bits == 4 ? run(cache_read_kernel<64, 4>) : run(cache_read_kernel<64, 8>);
