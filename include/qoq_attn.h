@@ -120,6 +120,9 @@ QOQ_API size_t qattn_paged_attention_workspace_bytes(int T, int B, int Hq, int H
  *              knows none). It only chooses kernels: rows beyond it are
  *              computed all the same.
  *   out        [T][Hq][d] FP16, row stride ldo.
+ * The call's rows times its longest context are limited: (T * Hq / 256 +
+ * min(T, B) * Hkv) * (table_pages * page_size / 128 + 2) < 2^31 (a table
+ * wider than the contexts need counts in full).
  *   workspace  any contents; calls that may run at the same time need one
  *              each. */
 QOQ_API int qattn_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d,

@@ -22,11 +22,10 @@ constexpr int kAnyRows = 1 << 30;
 struct Plan {
     bool rows, tiles;   // which kernels run
     int few;            // sequences with at most this many rows are the first one's
-    int splits;         // CTAs that share the keys of a row tile
     size_t rows_bytes, tiles_bytes;
 };
 
-Plan plan(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, int max_new)
+Plan plan(int T, int Hq, int Hkv, int d, int max_new)
 {
     const int G = Hq / Hkv;
     const int64_t most = (int64_t)std::min(max_new, T) * G;      // rows of a sequence, as far as the caller knows
@@ -34,16 +33,8 @@ Plan plan(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, 
     p.rows = G <= kFewRows;
     p.tiles = most > kFewRows;
     p.few = !p.rows ? 0 : p.tiles ? kFewRows : kAnyRows;
-    p.splits = 1;
-    if (p.tiles) {
-        // few row tiles leave SMs idle, or busy with a last one that sees a long context alone; a split costs its CTA's
-        // start and end (about as much as two key tiles) and the join
-        const int64_t ctas = std::max<int64_t>(1, row_tiles(T, B, G, p.few) * Hkv);
-        const int64_t keys = ((int64_t)table_pages * page_size + 127) / 128;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({148 / ctas, keys / 4, 16}));
-    }
     p.rows_bytes = p.rows ? (rows_workspace(d) + 15) & ~(size_t)15 : 0;
-    p.tiles_bytes = p.splits > 1 ? (size_t)p.splits * T * Hq * (d + 2) * sizeof(float) : 0;
+    p.tiles_bytes = p.tiles ? tiles_workspace(d) : 0;
     return p;
 }
 
@@ -62,9 +53,14 @@ int attn_sms()
     return n;
 }
 
-size_t paged_attention_workspace(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, int max_new)
+bool paged_attention_fits(int T, int B, int Hq, int Hkv, int table_pages, int page_size)
 {
-    const Plan p = plan(T, B, Hq, Hkv, d, table_pages, page_size, max_new);
+    return tiles_fit(row_tiles(T, B, Hq / Hkv, 0), Hkv, table_pages, page_size);
+}
+
+size_t paged_attention_workspace(int T, int Hq, int Hkv, int d, int max_new)
+{
+    const Plan p = plan(T, Hq, Hkv, d, max_new);
     return p.rows_bytes + p.tiles_bytes;
 }
 
@@ -72,15 +68,15 @@ cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq
                                    const AttnBatch &a, int max_new, float scale, uint16_t *out, int64_t ldo,
                                    void *workspace, cudaStream_t stream)
 {
-    const Plan p = plan(T, a.B, Hq, Hkv, d, a.table_pages, a.page_size, max_new);
+    const Plan p = plan(T, Hq, Hkv, d, max_new);
     if (p.rows) {
         const bool eight = (int64_t)std::min(max_new, T) * (Hq / Hkv) <= 8;
         const cudaError_t e = launch_paged_rows(q, ldq, T, Hq, Hkv, d, c, a, p.few, eight, scale, out, ldo, workspace, stream);
         if (e != cudaSuccess) return e;
     }
     if (!p.tiles) return cudaSuccess;
-    return launch_paged_tiles(q, ldq, T, Hq, Hkv, d, c, a, p.few, p.splits, scale, out, ldo,
-                              reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + p.rows_bytes), stream);
+    return launch_paged_tiles(q, ldq, T, Hq, Hkv, d, c, a, p.few, scale, out, ldo,
+                              reinterpret_cast<uint8_t *>(workspace) + p.rows_bytes, stream);
 }
 
 }  // namespace qoq

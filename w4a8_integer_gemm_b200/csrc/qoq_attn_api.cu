@@ -138,8 +138,8 @@ size_t qattn_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int 
 {
     if (!valid_counts(T, B) || !valid_heads(Hq, Hkv, d) || !valid_paging(page_size, 1, table_pages) || max_new < 1)
         return 0;
-    if (T == 0 || B == 0) return 0;
-    return qoq::paged_attention_workspace(T, B, Hq, Hkv, d, table_pages, page_size, max_new);
+    if (T == 0 || B == 0 || !qoq::paged_attention_fits(T, B, Hq, Hkv, table_pages, page_size)) return 0;
+    return qoq::paged_attention_workspace(T, Hq, Hkv, d, max_new);
 }
 
 int qattn_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const uint8_t *k_codes,
@@ -152,11 +152,12 @@ int qattn_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv
         max_new < 1 || !std::isfinite(scale))
         return QOQ_ERR_INVALID_ARG;
     if (T == 0 || B == 0) return QOQ_OK;
+    if (!qoq::paged_attention_fits(T, B, Hq, Hkv, table_pages, page_size)) return QOQ_ERR_INVALID_ARG;
     if (!valid_rows(q, ldq, Hq, d) || !valid_rows(out, ldo, Hq, d) ||
         !valid_cache(k_codes, v_codes, k_par, v_par, bits) || !valid_index(table) || !valid_index(cu) ||
         !valid_index(kv_len))
         return QOQ_ERR_INVALID_ARG;
-    const size_t need = qoq::paged_attention_workspace(T, B, Hq, Hkv, d, table_pages, page_size, max_new);
+    const size_t need = qoq::paged_attention_workspace(T, Hq, Hkv, d, max_new);
     if (workspace_bytes < need || (need && (!workspace || !aligned16(workspace)))) return QOQ_ERR_INVALID_ARG;
     const int dev = check_device();
     if (dev != QOQ_OK) return dev;

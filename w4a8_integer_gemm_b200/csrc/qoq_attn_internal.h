@@ -62,19 +62,23 @@ cudaError_t launch_cache_append(const uint16_t *k, int64_t ldk, const uint16_t *
 cudaError_t launch_cache_read(const AttnCache &c, const AttnBatch &a, int T, int Hkv, int d, uint16_t *K, uint16_t *V,
                               cudaStream_t stream);
 
-size_t paged_attention_workspace(int T, int B, int Hq, int Hkv, int d, int table_pages, int page_size, int max_new);
+// Whether the work of such a call can be counted in 31 bits.
+bool paged_attention_fits(int T, int B, int Hq, int Hkv, int table_pages, int page_size);
+size_t paged_attention_workspace(int T, int Hq, int Hkv, int d, int max_new);
 cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                    const AttnBatch &a, int max_new, float scale, uint16_t *out, int64_t ldo,
                                    void *workspace, cudaStream_t stream);
 // SMs of the current device, looked up once per device.
 int attn_sms();
-// Row tiles that a batch can have at most (sequences with more than `few` rows).
+// Row tiles that a batch can have at most (sequences with more than `few` rows), and whether their key tiles can be
+// counted in 31 bits.
 int64_t row_tiles(int T, int B, int G, int few);
-// Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows; with splits > 1 the
-// keys are shared by that many CTAs, which leave their sums in `part`.
+bool tiles_fit(int64_t tiles, int Hkv, int table_pages, int page_size);
+// Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows.
+size_t tiles_workspace(int d);
 cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
-                               const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
-                               float *part, cudaStream_t stream);
+                               const AttnBatch &a, int few, float scale, uint16_t *out, int64_t ldo, void *workspace,
+                               cudaStream_t stream);
 // Few rows (qoq_attn_rows.cu): the sequences with at most `few` rows, 8 rows (eight) or 16 to a pass over the cache.
 size_t rows_workspace(int d);
 cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,

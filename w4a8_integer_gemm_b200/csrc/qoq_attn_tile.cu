@@ -53,10 +53,11 @@ constexpr uint64_t kBudgetNs = 2000000000ull;
 
 __device__ int g_tile_error;        // non-zero after a bounded wait ran out
 
-// One work item: 256 rows of a sequence and KV head, and a share of its keys.
+// One work item: 256 rows of a sequence and KV head, and all or some of their keys.
 struct __align__(16) TileItem {
     int row0, rows;         // first row (new token * G + head of the group) in the sequence, rows from there on
-    int b, n, hk, split;    // sequence (-1: the list is at its end), its new tokens, KV head, share of the keys
+    int b, n, hk;           // sequence (-1: the list is at its end), its new tokens, KV head
+    int slot;               // where the CTA leaves a partial result: 0 or 1; -1: all keys, the result is final
     int t_seq, first;       // first row of the sequence in the batch, position of its new token 0
     int j0, cnt[2], steps;  // first key tile, key tiles of each row tile, of both
 };
@@ -67,7 +68,7 @@ struct TileMisc {
     float row[2][2][128];   // [row tile][half of the columns][row]: what the two threads of a row exchange
     TileItem item[kAhead];
     uint8_t chunk[kChunks]; // chunks, the one with the longest sequence first
-    int before[kChunks];    // row tiles before each of them
+    int before[kChunks];    // row tiles (a cache's: key tiles of row tiles and heads) before each of them
     int total;
     uint32_t tmem_slot;
     int abort_flag;
@@ -90,10 +91,12 @@ struct TileArgs {
     const uint16_t *q, *k, *v;
     int64_t ldq, ldk, ldv, ldo;
     uint16_t *out;
-    float *part;            // [splits][T * Hq][D] sums and, after them, [splits][T * Hq][2] (maximum, sum); null: no split
+    float *part;            // (a cache) [CTAs][2][256][D + 2]: sums of rows, then (maximum, sum of weights) of each
+    int4 *joined;           // (a cache) [CTAs]: (sequence or -1, first row, KV head, first CTA) of the row tile whose
+                            // keys end in the CTA's share and began in an earlier one's
     AttnCache c;
     AttnBatch a;
-    int T, Hq, Hkv, G, splits;
+    int T, Hq, Hkv, G;
     int few;                // sequences with at most this many rows (n_b * G) are another kernel's
     float scale_log2;       // |scale| * log2(e)
     uint32_t flip;          // 0x80008000 when scale < 0: the sign goes into q
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const bool failed = polls && !wait_short(bar, parity, &abort_flag, kBudgetNs);
         return !named_barrier_any(id, count, failed);
     };
-    // ---- the items: row tiles of all sequences x KV heads x shares of the keys, those that see most first ----
+    // ---- the items: row tiles of all sequences x KV heads, those that see most first ----
     // row tiles of sequence b (none if it is another kernel's, or has rows outside the batch)
     const int per_chunk = (p.a.B + kChunks - 1) / kChunks;
     auto tiles_of = [&](int b, int &n) -> int {
@@ -248,12 +251,26 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const int64_t r = (int64_t)n * p.G;
         return r > p.few ? (int)((r + kRows - 1) / kRows) : 0;
     };
+    // (a cache) key tiles that row tile `row0` of a sequence sees, at least one: even a row tile that sees nothing is
+    // worked on
+    auto units_of = [&](int first, int n, int row0) -> int {
+        const int r = min(n * p.G - row0, kRows) - 1;
+        const int keys = min(first + (row0 + r) / p.G + 1, p.a.table_pages * p.a.page_size);
+        return max(1, (keys + kKeys - 1) / kKeys);
+    };
+    auto first_of = [&](int b, int n) -> int { return max(0, __ldg(p.a.kv_len + b)) - n; };
     if (warp < kChunks / 32) {
         int *length = reinterpret_cast<int *>(misc.row);
         int sum = 0, n, len = 0;
         for (int b = threadIdx.x * per_chunk; b < min(p.a.B, ((int)threadIdx.x + 1) * per_chunk); ++b) {
-            sum += tiles_of(b, n);
+            const int tiles = tiles_of(b, n);
             len = max(len, BITS ? __ldg(p.a.kv_len + b) : n);
+            if (BITS) {
+                const int first = first_of(b, n);
+                for (int i = 0; i < tiles; ++i) sum += units_of(first, n, i * kRows) * p.Hkv;
+            } else {
+                sum += tiles;
+            }
         }
         length[threadIdx.x] = sum > 0 ? len : -1;
         named_barrier(1, kChunks);
@@ -426,57 +443,115 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             cp_async_wait<0>();
         }
         if (warp == kPlanWarp) {
-            const int items = misc.total * p.Hkv * p.splits;
-            bool more = true;
-            for (int k = 0; more; ++k) {
-                // (rounds go to and fro over the CTAs, since items get smaller)
-                const int x = k * (int)gridDim.x + (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-                more = x < items;
-                if (more) {
-                    w.split = x % p.splits;
-                    w.hk = x / p.splits % p.Hkv;
-                    int tile = x / p.splits / p.Hkv, count;
-                    int lo = 0, hi = kChunks - 1;    // the last chunk that begins at or before the tile
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (misc.before[mid] <= tile) lo = mid;
-                        else hi = mid - 1;
+            // the chunk of sequences that begins at or before place x of the list, with x counted from its beginning
+            auto chunk_at = [&](int &x) -> int {
+                int lo = 0, hi = kChunks - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (misc.before[mid] <= x) lo = mid;
+                    else hi = mid - 1;
+                }
+                x -= misc.before[lo];
+                return lo;
+            };
+            int emitted = 0;
+            // hands w over, with key tiles [j0, j1) of its rows; false when a wait ran out
+            auto emit = [&](int j1) -> bool {
+                if (w.b >= 0) {
+                    w.rows = w.n * p.G - w.row0;
+                    w.t_seq = __ldg(p.a.cu + w.b);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int r = min(w.rows, 128 * (t + 1)) - 1;
+                        int last = w.rows > 128 * t ? max(0, w.first + (w.row0 + r) / p.G + 1) : 0;   // keys its last row sees
+                        if (BITS) last = min(last, p.a.table_pages * p.a.page_size);
+                        w.cnt[t] = max(0, min((last + kKeys - 1) / kKeys, j1) - w.j0);
                     }
-                    tile -= misc.before[lo];
-                    for (w.b = misc.chunk[lo] * per_chunk;; ++w.b) {
+                    w.steps = max(w.cnt[0], w.cnt[1]);
+                }
+                const int i = emitted % kAhead;
+                if (emitted >= kAhead &&
+                    !__all_sync(0xffffffffu, wait_short(iempty(i), (uint32_t)(emitted / kAhead - 1) & 1, &abort_flag, kBudgetNs)))
+                    return false;
+                if (lane == 0) {
+                    misc.item[i] = w;
+                    mbar_arrive(ifull(i));
+                }
+                ++emitted;
+                return true;
+            };
+            bool ok = true;
+            if (BITS == 0) {
+                // whole row tiles, in rounds that go to and fro over the CTAs, since they get smaller
+                const int items = misc.total * p.Hkv;
+                for (int k = 0; ok; ++k) {
+                    const int x = k * (int)gridDim.x + (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+                    if (x >= items) break;
+                    w.hk = x % p.Hkv;
+                    w.slot = -1;
+                    w.j0 = w.first = 0;
+                    int tile = x / p.Hkv, count;
+                    for (w.b = misc.chunk[chunk_at(tile)] * per_chunk;; ++w.b) {
                         count = tiles_of(w.b, w.n);
                         if (tile < count) break;
                         tile -= count;
                     }
                     w.row0 = (count - 1 - tile) * kRows;
-                    w.rows = w.n * p.G - w.row0;
-                    w.t_seq = __ldg(p.a.cu + w.b);
-                    w.first = BITS ? max(0, __ldg(p.a.kv_len + w.b)) - w.n : 0;
-                    int last[2];                     // keys that the last row of each row tile sees, in key tiles
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int r = min(w.rows, 128 * (t + 1)) - 1;
-                        last[t] = w.rows > 128 * t ? max(0, w.first + (w.row0 + r) / p.G + 1) : 0;
-                        if (BITS) last[t] = min(last[t], p.a.table_pages * p.a.page_size);
-                        last[t] = (last[t] + kKeys - 1) / kKeys;
-                    }
-                    const int all = max(last[0], last[1]), j1 = all * (w.split + 1) / p.splits;
-                    w.j0 = all * w.split / p.splits;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) w.cnt[t] = max(0, min(last[t], j1) - w.j0);
-                    w.steps = max(w.cnt[0], w.cnt[1]);
-                } else {
-                    w.b = -1;
+                    ok = emit(1 << 30);
                 }
-                const int i = k % kAhead;
-                if (k >= kAhead &&
-                    !__all_sync(0xffffffffu, wait_short(iempty(i), (uint32_t)(k / kAhead - 1) & 1, &abort_flag, kBudgetNs)))
-                    break;
-                if (lane == 0) {
-                    misc.item[i] = w;
-                    mbar_arrive(ifull(i));
+            } else {
+                // An equal share of all key tiles: CTA c of P takes units c S / P .. (c + 1) S / P - 1 of the list of
+                // (row tile, head, key tile).  A row tile whose keys are shared out leaves a part in each CTA.
+                const int ctas = min((int)gridDim.x, misc.total), c = blockIdx.x;
+                if (lane == 0) p.joined[c] = make_int4(-1, 0, 0, 0);
+                int at = c < ctas ? (int)((int64_t)misc.total * c / ctas) : 0;
+                const int end = c < ctas ? (int)((int64_t)misc.total * (c + 1) / ctas) : 0;
+                if (at < end) {
+                    int x = at, lo = chunk_at(x), units = 0;
+                    int in_chunk = 0;
+                    // the first row tile: x becomes the place in it
+                    for (bool found = false; !found;) {
+                        w.b = misc.chunk[lo] * per_chunk + in_chunk;
+                        const int tiles = tiles_of(w.b, w.n);
+                        w.first = first_of(w.b, w.n);
+                        for (w.row0 = (tiles - 1) * kRows; w.row0 >= 0; w.row0 -= kRows) {
+                            units = units_of(w.first, w.n, w.row0);
+                            found = x < units * p.Hkv;
+                            if (found) break;
+                            x -= units * p.Hkv;
+                        }
+                        if (!found) ++in_chunk;
+                    }
+                    w.hk = x / units;
+                    w.j0 = x % units;
+                    while (ok) {
+                        const int j1 = min(units, w.j0 + end - at);
+                        w.slot = w.j0 == 0 && j1 == units ? -1 : w.j0 == 0 ? 1 : 0;
+                        if (w.slot == 0 && j1 == units && lane == 0)
+                            p.joined[c] = make_int4(w.b, w.row0, w.hk,
+                                                    (int)(((int64_t)(at - w.j0 + 1) * ctas - 1) / misc.total));
+                        ok = emit(j1);
+                        at += j1 - w.j0;
+                        if (at >= end) break;
+                        w.j0 = 0;
+                        if (++w.hk < p.Hkv) continue;
+                        w.hk = 0;
+                        w.row0 -= kRows;
+                        while (w.row0 < 0) {                 // the next sequence with tiles
+                            if (++in_chunk == per_chunk || misc.chunk[lo] * per_chunk + in_chunk >= p.a.B) {
+                                in_chunk = 0;
+                                ++lo;
+                            }
+                            w.b = misc.chunk[lo] * per_chunk + in_chunk;
+                            w.row0 = w.b < p.a.B ? (tiles_of(w.b, w.n) - 1) * kRows : -1;
+                            w.first = w.b < p.a.B ? first_of(w.b, w.n) : 0;
+                        }
+                        units = units_of(w.first, w.n, w.row0);
+                    }
                 }
             }
+            w.b = -1;
+            if (ok) emit(0);
         }
         if (BITS == 0 && warp == 16) {
             // TMA, except for the last values of a sequence: rows behind it are another's, or nobody's, and may hold
@@ -739,7 +814,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             named_barrier(4 + t, 256);
             l = s_row[t][0][r] + s_row[t][1][r];
             const int g = real ? (w.row0 + row) % p.G : 0;
-            if (p.part == nullptr) {
+            if (BITS == 0 || w.slot < 0) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 uint16_t *dst = p.out + (int64_t)(w.t_seq + tok) * p.ldo + (size_t)(w.hk * p.G + g) * D + kOut * h;
 #pragma unroll
@@ -766,12 +841,9 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                 }
             } else {
-                const int64_t all_rows = (int64_t)p.T * p.Hq, orow = (int64_t)(w.t_seq + tok) * p.Hq + w.hk * p.G + g;
-                float *dst = p.part + ((int64_t)w.split * all_rows + orow) * D + kOut * h;
-                if (real && h == 0) {
-                    float2 *ml = reinterpret_cast<float2 *>(p.part + (int64_t)p.splits * all_rows * D);
-                    ml[(int64_t)w.split * all_rows + orow] = make_float2(m, l);
-                }
+                float *mine = p.part + ((size_t)blockIdx.x * 2 + w.slot) * kRows * (D + 2);
+                float *dst = mine + row * D + kOut * h;
+                if (h == 0) reinterpret_cast<float2 *>(mine + kRows * D)[row] = make_float2(m, l);
 #pragma unroll
                 for (int c = 0; c < (w.cnt[t] > 0 ? kOut : 0); c += 16) {
                     uint32_t o[16];
@@ -795,42 +867,46 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     }
     tc_fence_before();
     __syncthreads();
+    if (BITS) grid_launch_dependents();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0 && abort_flag) atomicExch(&g_tile_error, 1);
 }
 
-// Joins the splits of a cache's row tiles: a warp per (row, query head), in order.
+// Joins a cache's row tiles that several CTAs share: CTA (x, y) the one that ended in CTA x's share, eight rows of it,
+// one per warp; the parts in order.
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_split_join_kernel(const float *__restrict__ part, int splits,
-                                                                          AttnBatch a, int T, int Hq, int G, int few,
-                                                                          uint16_t *__restrict__ out, int64_t ldo)
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_tile_join_kernel(const float *__restrict__ part,
+                                                                         const int4 *__restrict__ joined, AttnBatch a,
+                                                                         int Hkv, int G, uint16_t *__restrict__ out, int64_t ldo)
 {
-    const int64_t rows = (int64_t)T * Hq, row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int lane = threadIdx.x & 31, t = (int)(row / Hq), h = (int)(row % Hq);
-    const int b = sequence_of(a.cu, a.B, t);
-    if (b < 0) return;
-    const int t0 = __ldg(a.cu + b), t1 = __ldg(a.cu + b + 1);
-    if (t0 < 0 || t1 > T || (int64_t)(t1 - t0) * G <= few) return;       // not the tiles' (find_tile)
-    const float2 *ml = reinterpret_cast<const float2 *>(part + (int64_t)splits * rows * D) + row;
+    grid_dependency_wait();
+    const int last = blockIdx.x, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 j = joined[last];
+    if (j.x < 0) return;
+    const int t0 = __ldg(a.cu + j.x), n = __ldg(a.cu + j.x + 1) - t0;
+    if (row >= n * G - j.y) return;
     constexpr int kN = D / 32;
     float M = -INFINITY, L = 0.0f, v[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[i] = 0.0f;
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, ml[s * rows].x);
-    for (int s = 0; s < splits; ++s) {
-        const float2 x = ml[s * rows];
-        if (x.y <= 0.0f) continue;                                       // saw nothing, wrote nothing
-        const float f = ex2(x.x - M);
-        L = fmaf(x.y, f, L);
-        const float *src = part + (s * rows + row) * D + kN * lane;
+    for (int c = j.w; c <= last; ++c) {
+        const float *src = part + ((size_t)c * 2 + (c == j.w ? 1 : 0)) * kRows * (D + 2);
+        const float2 ml = reinterpret_cast<const float2 *>(src + kRows * D)[row];
+        float x[kN];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = fmaf(src[i], f, v[i]);
+        for (int i = 0; i < kN; ++i) x[i] = src[row * D + kN * lane + i];
+        if (ml.y <= 0.0f) continue;                  // saw nothing, and wrote no sums
+        const float m1 = fmaxf(M, ml.x), f0 = M == -INFINITY ? 0.0f : ex2(M - m1), f1 = ex2(ml.x - m1);
+        M = m1;
+        L = fmaf(L, f0, ml.y * f1);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = fmaf(v[i], f0, x[i] * f1);
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    uint16_t *dst = out + t * ldo + (size_t)h * D + kN * lane;
+    const int r = j.y + row;
+    uint16_t *dst = out + (int64_t)(t0 + r / G) * ldo + (size_t)(j.z * G + r % G) * D + kN * lane;
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {
         const __half2 x = __floats2half2_rn(v[i] * inv, v[i + 1] * inv);
@@ -838,16 +914,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_split_join_kernel(const 
     }
 }
 
+constexpr int kMaxTileCtas = 160;       // sizes the workspace
+
 template <int D, int BITS>
 cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
 {
     auto kernel = attn_tile_kernel<D, BITS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    // one CTA per SM (shared and tensor memory allow no more), each with its share of the items
-    const int64_t items = row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * p.splits;
-    kernel<<<(unsigned)std::min<int64_t>(items, attn_sms()), tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
-    return cudaGetLastError();
+    // one CTA per SM (shared and tensor memory allow no more), each with its share of the work
+    const int64_t items = BITS ? row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * 64 : row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv;
+    const int ctas = (int)std::min<int64_t>(items, std::min(attn_sms(), kMaxTileCtas));
+    kernel<<<ctas, tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
+    if (BITS == 0) return cudaGetLastError();
+    const cudaError_t e1 = cudaGetLastError();
+    if (e1 != cudaSuccess) return e1;
+    // the join's CTAs come up as the others end, and wait for the last
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, kRows / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tile_join_kernel<D>, (const float *)p.part, (const int4 *)p.joined, p.a, p.Hkv, p.G,
+                              p.out, p.ldo);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -908,7 +1001,7 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream)
 {
-    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 1, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
+    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
     cudaError_t e = encode_rows(&p.map_k, k, T, Hkv * d, ldk);
     if (e == cudaSuccess) e = encode_rows(&p.map_v, v, T, Hkv * d, ldv);
@@ -916,20 +1009,26 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
     return d == 128 ? launch_tile<128, 0>(p, stream) : launch_tile<64, 0>(p, stream);
 }
 
-cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
-                               const AttnBatch &a, int few, int splits, float scale, uint16_t *out, int64_t ldo,
-                               float *part, cudaStream_t stream)
+size_t tiles_workspace(int d)
 {
-    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, part, c, a, T, Hq, Hkv, Hq / Hkv, splits, few, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
+    return (size_t)kMaxTileCtas * (sizeof(int4) + 2 * kRows * (d + 2) * sizeof(float));
+}
+
+bool tiles_fit(int64_t tiles, int Hkv, int table_pages, int page_size)
+{
+    return tiles * Hkv * ((int64_t)table_pages * page_size / kKeys + 2) < ((int64_t)1 << 31);
+}
+
+cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
+                               const AttnBatch &a, int few, float scale, uint16_t *out, int64_t ldo, void *workspace,
+                               cudaStream_t stream)
+{
+    int4 *joined = reinterpret_cast<int4 *>(workspace);
+    TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, reinterpret_cast<float *>(joined + kMaxTileCtas), joined, c, a, T, Hq,
+               Hkv, Hq / Hkv, few, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
-    if (splits == 1) p.part = nullptr;
-    const cudaError_t e = d == 128 ? (c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream))
-                                   : (c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream));
-    if (e != cudaSuccess || splits == 1) return e;
-    const unsigned grid = (unsigned)(((int64_t)T * Hq + kJoinWarps - 1) / kJoinWarps);
-    auto join = d == 128 ? attn_split_join_kernel<128> : attn_split_join_kernel<64>;
-    join<<<grid, 32 * kJoinWarps, 0, stream>>>(part, splits, a, T, Hq, Hq / Hkv, few, out, ldo);
-    return cudaGetLastError();
+    if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream);
+    return c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream);
 }
 
 cudaError_t read_and_clear_tile_error(int *value)
