@@ -15,7 +15,7 @@
 //                    (tensor memory) rescaled; at the end O to HBM.
 //   loaders          keys and values of the tile into a ring of shared-memory
 //                    slots in the 128-byte-swizzled layout: a warp with TMA
-//                    for FP16 rows; for a cache two warpgroups that expand
+//                    for FP16 rows; for a cache a warpgroup that expands
 //                    the codes to fp16(s c + m) in registers.
 //   the last         one thread issues the MMAs: S = Q K^T (both from shared
 //                    memory), O += P V (P from tensor memory, V with its
@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -44,9 +45,9 @@
 namespace qoq {
 namespace {
 
-// Threads: four softmax warpgroups; for prompts one more with the loader's and the MMA issuer's warp, for a cache two
-// loaders (keys, values) and the MMA issuer's.
-__host__ __device__ constexpr int tile_threads(int bits) { return bits ? 896 : 640; }
+// Threads: four softmax warpgroups, for a cache one that loads, and one with the other roles' warps.  (A cache with two
+// loaders, keys and values, leaves the softmax 88 registers instead of 96, and one buffer for S: 4% slower.)
+__host__ __device__ constexpr int tile_threads(int bits) { return bits ? 768 : 640; }
 constexpr int kRows = 256;          // rows of a CTA (two tiles of 128)
 constexpr int kKeys = 128;          // keys of a tile
 constexpr uint64_t kBudgetNs = 2000000000ull;
@@ -181,11 +182,11 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 896 with 72.
+// Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 768 with 80.
 template <int BITS>
 struct Regs {
-    static constexpr int kSoftmax = BITS ? 88 : 104, kLoader = BITS ? 56 : 0, kRest = BITS ? 40 : 64;
-    static_assert(512 * kSoftmax + (BITS ? 256 * kLoader : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 72 : 96), "register split");
+    static constexpr int kSoftmax = BITS ? 96 : 104, kLoader = BITS ? 56 : 0, kRest = BITS ? 40 : 64;
+    static_assert(512 * kSoftmax + (BITS ? 128 * kLoader : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 80 : 96), "register split");
 };
 
 // BITS 0: FP16 rows of the batch itself (prompts); 4 or 8: the cache.
@@ -193,8 +194,8 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const __grid_constant__ TileArgs p)
 {
     using C = TileCfg<D>;
-    constexpr int kMmaWarp = BITS ? 24 : 17, kQWarp = kMmaWarp + 1, kQWarps = BITS ? 2 : 1;
-    constexpr int kPlanWarp = kQWarp + kQWarps, kReaders = 16 + 1 + kQWarps + (BITS ? 8 : 1);   // warps that read items
+    constexpr int kMmaWarp = BITS ? 20 : 17, kQWarp = kMmaWarp + 1, kQWarps = BITS ? 2 : 1;
+    constexpr int kPlanWarp = kQWarp + kQWarps, kReaders = 16 + 1 + kQWarps + (BITS ? 4 : 1);   // warps that read items
     extern __shared__ __align__(1024) uint8_t smem[];
     TileMisc &misc = *reinterpret_cast<TileMisc *>(smem + C::kMisc);
     int &abort_flag = misc.abort_flag;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         return w.b >= 0;
     };
 
-    if (BITS ? warp >= 24 : warp >= 16) {
+    if (BITS ? warp >= 20 : warp >= 16) {
         // ------------------------------------- MMA (and the prompts' loader) --
         regs_down<Regs<BITS>::kRest>();
         if (warp == kMmaWarp) {
@@ -601,17 +602,14 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         // ------------------------------------------------ loaders of a cache --
         regs_down<Regs<BITS ? BITS : 4>::kLoader>();
         {
-            // One warpgroup brings the keys, the other the values.  kLanes lanes share a row's bytes, 16 each; a thread's
+            // One warpgroup brings the keys and the values in turn.  kLanes lanes share a row's bytes, 16 each; a thread's
             // kLanes rows lie in one granule of 16 tokens, kGap apart, so one page and constant offsets serve them.
             constexpr int kB = BITS ? BITS : 4;
             constexpr int kRowBytes = D * kB / 8, kLanes = kRowBytes / 16, kGap = 16 / kLanes;
             constexpr int kVecs = 128 / kB / 8;                      // 16-byte vectors of 8 channels from 16 bytes of codes
-            const bool val = warp >= 20;
             const int tid = threadIdx.x & 127, part = tid % kLanes;
             const int r0 = 16 * (tid / 16) + tid % 16 / kLanes;      // r0 % 8 is below kGap, and the other rows' r % 8 are
                                                                      // r0 % 8 ^ (kGap i % 8)
-            const uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + part * 16;
-            const uint32_t *pars = reinterpret_cast<const uint32_t *>(val ? p.c.v_par : p.c.k_par);
             constexpr int kBatch = kLanes < 4 ? kLanes : 4, kBatches = kLanes / kBatch;    // rows in registers at a time
             uint4 c[kBatch];
             uint32_t pr[kBatch];
@@ -620,12 +618,13 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 const int pos = (w.j0 + step) * kKeys + r0;
                 page = (pos & ~15) < w.first + w.n ? page_of(p.a, w.b, pos) : -1;
             };
-            auto fetch = [&](int step, int batch) {
+            auto fetch = [&](int u, int batch) {                     // u: keys (even) and values (odd) of the steps
+                const int step = u >> 1;
                 const int pos = (w.j0 + step) * kKeys + r0 + batch * kBatch * kGap, end = w.first + w.n;
                 // (a pool of 2^32 rows would not fit the GPU)
                 const uint32_t row = ((uint32_t)page * p.Hkv + w.hk) * p.a.page_size + (pos & (p.a.page_size - 1));
-                const uint8_t *src = codes + (size_t)row * kRowBytes;
-                const uint32_t *par = pars + row;
+                const uint8_t *src = (u & 1 ? p.c.v_codes : p.c.k_codes) + part * 16 + (size_t)row * kRowBytes;
+                const uint32_t *par = reinterpret_cast<const uint32_t *>(u & 1 ? p.c.v_par : p.c.k_par) + row;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     c[i] = make_uint4(0, 0, 0, 0);
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         pr[i] = __ldg(par + kGap * i);
                     }
                 }
-                if (batch == kBatches - 1) look_up(step + 1);
+                if ((u & 1) && batch == kBatches - 1) look_up(step + 1);
             };
             // Vector v of the thread's codes is vector kVecs * part + v of the row.  Lanes of the row's upper half store
             // theirs in another order, so that eight lanes meet eight bank groups.
@@ -664,16 +663,16 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
             };
             static_assert(kBatches == 1 || kBatch * kGap % 8 == 0, "swizzle of the batches");
-            int unit = val;
+            int unit = 0;
             bool ok = true;
             while (ok && get()) {
                 if (w.steps == 0) continue;
                 look_up(0);
                 fetch(0, 0);
-                for (int i = 0; i < w.steps; ++i, unit += 2) {
+                for (int i = 0; i < 2 * w.steps; ++i, ++unit) {
                     const int slot = unit % C::kSlots;
                     ok = unit < C::kSlots ||
-                         group_wait(6 + val, 128, (warp & 3) == 0, empty(slot), (uint32_t)(unit / C::kSlots - 1) & 1);
+                         group_wait(6, 128, (warp & 3) == 0, empty(slot), (uint32_t)(unit / C::kSlots - 1) & 1);
                     if (!ok) break;
 #pragma unroll
                     for (int x = 0; x < kBatches; ++x) {
@@ -683,7 +682,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(slot));
-                    if (i + 1 < w.steps) fetch(i + 1, 0);
+                    if (i + 1 < 2 * w.steps) fetch(i + 1, 0);
                 }
             }
         }
@@ -699,19 +698,29 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const uint32_t tp = tmem + 128 * t + kCols / 2 * h + lanes;
         const uint32_t to = tmem + 256 + D * t + kOut * h + lanes;
         const float sl = p.scale_log2;
+        const int mates = 8 + 4 * t + (warp & 3);                    // barrier of the two warps that share 32 rows
         int used = 0, finished = 0;                                  // uses of sfull, of ofull
         bool ok = true;
         while (ok && get()) {
         const bool real = row < w.rows;
         const int tok = real ? (w.row0 + row) / p.G : 0;
         const int see = real ? w.first + tok + 1 : 0;                // keys 0 .. see - 1 are seen
-        const int see_min = __reduce_min_sync(0xffffffffu, see);
+        const int see_min = __reduce_min_sync(0xffffffffu, real ? see : INT_MAX);   // (what other rows come to is not used)
         float m = -INFINITY, l = 0.0f;                               // maximum in use (log2 units), sum of the columns
+        // (a cache) the table's entry for a 16-token piece of step i's columns, a lane each; fetched a step ahead
+        auto piece = [&](int i) {
+            const int place = ((w.j0 + i) * kKeys + kCols * h + 16 * lane) >> p.a.page_shift;
+            return BITS && lane < 4 && place < p.a.table_pages ? __ldg(p.a.table + (size_t)w.b * p.a.table_pages + place) : -1;
+        };
+        int page = piece(0);
         for (int i = 0; i < w.cnt[t]; ++i) {
             const int key0 = (w.j0 + i) * kKeys + kCols * h;
             // (cache) which 16-token pieces of the columns are there
             uint32_t there = 0xFu;
-            if (BITS) there = __ballot_sync(0xffffffffu, lane < 4 && page_of(p.a, w.b, key0 + 16 * lane) >= 0);
+            if (BITS) {
+                there = __ballot_sync(0xffffffffu, page >= 0 && page < p.a.pages);
+                page = piece(i + 1);
+            }
             ok = group_wait(2 + t, 256, (warp & 7) == 0, sfull(t), (uint32_t)used++ & 1);
             if (!ok) break;
             tc_fence_after();
@@ -726,49 +735,48 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             };
             // P = 2^(s - m), FP16, with the maximum in use, 16 columns at a time, the next 16 on their way from tensor
             // memory.  The maximum may lag far behind: as long as a thread's weights sum to at most 2^14 they fit FP16,
-            // and no maximum has to be taken.  Otherwise, and for the first keys that a row sees, the row tile's warps
-            // take it, rescale what they have and weigh the tile again.
+            // and no maximum has to be taken.  Otherwise, and for the first keys that a row sees, the two warps of the
+            // rows take it, rescale what they have and weigh the tile again.
             uint32_t pk[kCols / 2];
             for (int round = 0;; ++round) {
-                const float sub = m == -INFINITY ? 0.0f : -m;
-                const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
-                uint64_t sum2[2] = {0, 0};
-                float high = -INFINITY;
-                // (a cache's loaders leave registers for one buffer only)
-                constexpr int kBuf = BITS ? 1 : 2;
-                uint32_t x[kBuf][16];
-                if (kBuf == 2) tmem_ld16_async(ts, x[0]);
+                if (round > 0 || i > 0) {                            // (an item's first keys have no maximum to use)
+                    const float sub = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t sl2 = pair(sl, sl), sub2 = pair(sub, sub);
+                    uint64_t sum2[2] = {0, 0};
+                    float high = -INFINITY;
+                    uint32_t x[2][16];
+                    tmem_ld16_async(ts, x[0]);
 #pragma unroll
-                for (int c0 = 0; c0 < kCols; c0 += 16) {
-                    uint32_t (&y)[16] = x[c0 / 16 % kBuf];
-                    if (kBuf == 1) tmem_ld16_async(ts + c0, y);
-                    tmem_wait_ld16(y);
-                    if (kBuf == 2 && c0 + 16 < kCols) tmem_ld16_async(ts + c0 + 16, x[(c0 / 16 + 1) % kBuf]);
-                    if (masked) mask(y, c0);
+                    for (int c0 = 0; c0 < kCols; c0 += 16) {
+                        uint32_t (&y)[16] = x[c0 / 16 % 2];
+                        tmem_wait_ld16(y);
+                        if (c0 + 16 < kCols) tmem_ld16_async(ts + c0 + 16, x[(c0 / 16 + 1) % 2]);
+                        if (masked) mask(y, c0);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(y[2 * u]), __uint_as_float(y[2 * u + 1])), sl2, sub2), e0, e1);
-                        if (BITS == 0 && u < kPoly) {
-                            high = fmaxf(fmaxf(high, e0), e1);       // (a sum would not show what is out of its range)
-                            ex2_pair(e0, e1);
-                        } else {
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
+                        for (int u = 0; u < 8; ++u) {
+                            float e0, e1;
+                            unpair(fma2(pair(__uint_as_float(y[2 * u]), __uint_as_float(y[2 * u + 1])), sl2, sub2), e0, e1);
+                            if (BITS == 0 && u < kPoly) {
+                                high = fmaxf(fmaxf(high, e0), e1);       // (a sum would not show what is out of its range)
+                                ex2_pair(e0, e1);
+                            } else {
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                            }
+                            sum2[u & 1] = add2(sum2[u & 1], pair(e0, e1));
+                            const __half2 x2 = __floats2half2_rn(e0, e1);
+                            pk[c0 / 2 + u] = *reinterpret_cast<const uint32_t *>(&x2);
                         }
-                        sum2[u & 1] = add2(sum2[u & 1], pair(e0, e1));
-                        const __half2 x2 = __floats2half2_rn(e0, e1);
-                        pk[c0 / 2 + u] = *reinterpret_cast<const uint32_t *>(&x2);
                     }
-                }
-                float s0, s1;
-                unpair(add2(sum2[0], sum2[1]), s0, s1);
-                s0 += s1;
-                // (also: everyone has read S before anyone writes P over it)
-                const bool again = named_barrier_any(4 + t, 256, round == 0 && (s0 > 16384.0f || high > 14.0f || (m == -INFINITY && lim > 0)));
-                if (!again) {
-                    l += s0;
-                    break;
+                    float s0, s1;
+                    unpair(add2(sum2[0], sum2[1]), s0, s1);
+                    s0 += s1;
+                    // (also: everyone has read S before anyone writes P over it)
+                    const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 16384.0f || high > 14.0f || (m == -INFINITY && lim > 0)));
+                    if (!again) {
+                        l += s0;
+                        break;
+                    }
                 }
                 float top = -INFINITY;
 #pragma unroll 1
@@ -780,7 +788,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     for (int c = 0; c < 16; ++c) top = fmaxf(top, __uint_as_float(y[c]));
                 }
                 s_row[t][h][r] = top * sl;
-                named_barrier(4 + t, 256);
+                named_barrier(mates, 64);
                 const float m1 = fmaxf(m, fmaxf(s_row[t][0][r], s_row[t][1][r]));
                 const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
                 m = m1;
@@ -794,7 +802,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
                     tmem_st16(to + c, o);
                 }
-                named_barrier(4 + t, 256);       // s_row has been read
+                named_barrier(mates, 64);       // s_row has been read
             }
             tmem_st32(tp, pk);
             tmem_wait_st();
@@ -811,7 +819,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         }
         {
             s_row[t][h][r] = l;
-            named_barrier(4 + t, 256);
+            named_barrier(mates, 64);
             l = s_row[t][0][r] + s_row[t][1][r];
             const int g = real ? (w.row0 + row) % p.G : 0;
             if (BITS == 0 || w.slot < 0) {
@@ -842,7 +850,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
             } else {
                 float *mine = p.part + ((size_t)blockIdx.x * 2 + w.slot) * kRows * (D + 2);
-                float *dst = mine + row * D + kOut * h;
+                float4 *dst = reinterpret_cast<float4 *>(mine) + kOut / 4 * h * kRows + row;
                 if (h == 0) reinterpret_cast<float2 *>(mine + kRows * D)[row] = make_float2(m, l);
 #pragma unroll
                 for (int c = 0; c < (w.cnt[t] > 0 ? kOut : 0); c += 16) {
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                             // columns 8v .. 8v + 7 hold channels 0 4 1 5 2 6 3 7 of a 4-bit cache
                             uint4 y = make_uint4(x[4 * (u & 1)], x[4 * (u & 1) + 1], x[4 * (u & 1) + 2], x[4 * (u & 1) + 3]);
                             if (BITS == 4) y = make_uint4(x[u & 1], x[2 + (u & 1)], x[4 + (u & 1)], x[6 + (u & 1)]);
-                            reinterpret_cast<uint4 *>(dst)[c / 4 + u] = y;
+                            reinterpret_cast<uint4 *>(dst)[(c / 4 + u) * kRows] = y;
                         }
                     }
                 }
@@ -873,45 +881,38 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
 }
 
 // Joins a cache's row tiles that several CTAs share: CTA (x, y) the one that ended in CTA x's share, eight rows of it,
-// one per warp; the parts in order.
-constexpr int kJoinWarps = 8;
+// four channels per thread; the parts in order.  A part holds four channels of all rows, then the next four: what the
+// warps that write it (a row per thread) and those that read it here take in whole lines.
+constexpr int kJoinRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_tile_join_kernel(const float *__restrict__ part,
-                                                                         const int4 *__restrict__ joined, AttnBatch a,
-                                                                         int Hkv, int G, uint16_t *__restrict__ out, int64_t ldo)
+__global__ void __launch_bounds__(kJoinRows *D / 4) attn_tile_join_kernel(const float *__restrict__ part,
+                                                                          const int4 *__restrict__ joined, AttnBatch a,
+                                                                          int Hkv, int G, uint16_t *__restrict__ out, int64_t ldo)
 {
     grid_dependency_wait();
-    const int last = blockIdx.x, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int last = blockIdx.x, row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, at = threadIdx.x / kJoinRows;
     const int4 j = joined[last];
     if (j.x < 0) return;
     const int t0 = __ldg(a.cu + j.x), n = __ldg(a.cu + j.x + 1) - t0;
     if (row >= n * G - j.y) return;
-    constexpr int kN = D / 32;
-    float M = -INFINITY, L = 0.0f, v[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+    float M = -INFINITY, L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c = j.w; c <= last; ++c) {
         const float *src = part + ((size_t)c * 2 + (c == j.w ? 1 : 0)) * kRows * (D + 2);
         const float2 ml = reinterpret_cast<const float2 *>(src + kRows * D)[row];
-        float x[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = src[row * D + kN * lane + i];
+        const float4 x = reinterpret_cast<const float4 *>(src)[at * kRows + row];
         if (ml.y <= 0.0f) continue;                  // saw nothing, and wrote no sums
         const float m1 = fmaxf(M, ml.x), f0 = M == -INFINITY ? 0.0f : ex2(M - m1), f1 = ex2(ml.x - m1);
         M = m1;
         L = fmaf(L, f0, ml.y * f1);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = fmaf(v[i], f0, x[i] * f1);
+        v = make_float4(fmaf(v.x, f0, x.x * f1), fmaf(v.y, f0, x.y * f1), fmaf(v.z, f0, x.z * f1), fmaf(v.w, f0, x.w * f1));
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const int r = j.y + row;
-    uint16_t *dst = out + (int64_t)(t0 + r / G) * ldo + (size_t)(j.z * G + r % G) * D + kN * lane;
-#pragma unroll
-    for (int i = 0; i < kN; i += 2) {
-        const __half2 x = __floats2half2_rn(v[i] * inv, v[i + 1] * inv);
-        *reinterpret_cast<__half2 *>(dst + i) = x;
-    }
+    uint16_t *dst = out + (int64_t)(t0 + r / G) * ldo + (size_t)(j.z * G + r % G) * D + 4 * at;
+    const __half2 y0 = __floats2half2_rn(v.x * inv, v.y * inv), y1 = __floats2half2_rn(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
 }
 
 constexpr int kMaxTileCtas = 160;       // sizes the workspace
@@ -931,8 +932,8 @@ cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
     if (e1 != cudaSuccess) return e1;
     // the join's CTAs come up as the others end, and wait for the last
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, kRows / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3(ctas, kRows / kJoinRows);
+    cfg.blockDim = dim3(kJoinRows * D / 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
