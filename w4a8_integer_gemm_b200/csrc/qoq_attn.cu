@@ -1,12 +1,14 @@
 // qoq_attn.cu -- attention of new tokens over the paged cache: which kernel
 // takes which sequence.
 //
-// A sequence has n_b * G rows per KV head.  Up to kFewRows of them fit one
-// pass of the kernel that streams the cache through warp-level MMAs
+// A sequence has n_b * G rows per KV head.  Up to kFewRows of them go to the
+// kernel that streams the cache through warp-level MMAs, sixteen rows a pass
 // (qoq_attn_rows.cu, bound by the cache's bytes); more go to the tensor-core
-// tiles (qoq_attn_tile.cu).  Each kernel looks at the lengths on the device
-// and skips the other's sequences, so a mixed batch takes both launches and
-// no length is read on the host.  The caller's max_new saves a launch.
+// tiles (qoq_attn_tile.cu).  32 sequences of 2000 tokens, 8 KV heads of 128
+// in 4 bits, us: 16 rows 41 against 77 in tiles, 32 rows 62 against 81.
+// Each kernel looks at the lengths on the device and skips the other's
+// sequences, so a mixed batch takes both launches and no length is read on
+// the host.  The caller's max_new saves a launch.
 #include <algorithm>
 #include <atomic>
 
@@ -16,7 +18,7 @@ namespace qoq {
 
 namespace {
 
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 32;
 constexpr int kAnyRows = 1 << 30;
 
 struct Plan {
@@ -70,6 +72,7 @@ cudaError_t launch_paged_attention(const uint16_t *q, int64_t ldq, int T, int Hq
 {
     const Plan p = plan(T, Hq, Hkv, d, max_new);
     if (p.rows) {
+        // rows in one column block of the MMAs instead of two: 45 us against 58 for 32 sequences of 4000 tokens
         const bool eight = (int64_t)std::min(max_new, T) * (Hq / Hkv) <= 8;
         const cudaError_t e = launch_paged_rows(q, ldq, T, Hq, Hkv, d, c, a, p.few, eight, scale, out, ldo, workspace, stream);
         if (e != cudaSuccess) return e;

@@ -5,10 +5,11 @@
 // Mathematics: one pass over the keys with the running maximum and sum of
 // the softmax, O = sum_j exp(s_j - m) v_j, out = O / sum_j exp(s_j - m).
 //
-// A CTA owns 256 rows of one sequence and KV head: row = (new token, query
+// A work item is 256 rows of one sequence and KV head: row = (new token, query
 // head of the group), so the heads that share a KV head share its tiles and
 // any group size fills the tile.  Two row tiles of 128 are in flight: while
 // one's softmax runs on the CUDA cores the tensor cores work for the other.
+// One CTA per SM stays and works through a list of items:
 //   warps 0-7, 8-15  softmax of row tile 0 and 1, two threads to a row: S from
 //                    tensor memory, masks, exp2, P as FP16 back to tensor
 //                    memory over S; now and then a new maximum, and O
@@ -17,11 +18,28 @@
 //                    slots in the 128-byte-swizzled layout: a warp with TMA
 //                    for FP16 rows; for a cache a warpgroup that expands
 //                    the codes to fp16(s c + m) in registers.
-//   the last         one thread issues the MMAs: S = Q K^T (both from shared
-//                    memory), O += P V (P from tensor memory, V with its
-//                    channels contiguous).
+//   MMA              S = Q K^T (both from shared memory), O += P V (P from
+//                    tensor memory, V with its channels contiguous).
+//   Q                the next item's Q as soon as the last S of this one is
+//                    done.
+//   plan             the list, a few items ahead, in a ring of descriptions.
 // Tensor memory: S0 S1 (128 columns each, P over the first half), O0 O1 (D
 // columns each).
+//
+// Lists.  Prompts: whole items, those that see most first, dealt to and fro
+// over the CTAs.  A cache: the line of all (item, key tile) is cut into equal
+// shares, one per CTA; an item that spans CTAs leaves a part in each, and a
+// second kernel joins them.  (Whole items, and keys cut into equal numbers of
+// tiles per item: chunks of 450 to 600 tokens over up to 13600 255 us against
+// 235, a mixed batch of short chunks 94 us against 75.)
+//
+// Bound: for each row tile a step is a chain, softmax (about 1300 cycles of
+// its 16 warps' exponentials and conversions, 900 of waits and stores) and
+// then 1060 cycles of MMAs, which run one after the other because P lies over
+// S and tensor memory has no room for a second S beside O; two row tiles fill
+// a period of 3340 cycles (a cache: 3900) with 2080 of MMAs.  Measured: a
+// prompt of 8192 tokens, 32 heads of 128: 500 us, 1.1 PFLOP/s, 66% of cuBLAS;
+// prompts of 1 to 1800 tokens, 16 heads: 153 us.
 //
 // Roundings below FP32: P (FP16, as the tensor core's operand: half a step of
 // each weight; the sum of weights is taken before it, in FP32) and, for a
@@ -103,7 +121,7 @@ struct TileArgs {
     uint32_t flip;          // 0x80008000 when scale < 0: the sign goes into q
     uint32_t e6, e5;        // 0x64006400, 0x54005400 (expand4)
     bool wide;              // out's rows begin on 32-byte boundaries: half as many store instructions, which the
-                            // load/store unit takes line by line
+                            // load/store unit takes line by line (packed prompts 153 us against 165)
     CUtensorMap map_k, map_v;   // (prompts) [T][Hkv * D], boxes of 64 channels x 128 rows, 128-byte swizzle
 };
 
@@ -161,7 +179,8 @@ __device__ __forceinline__ void ex2_pair(float &x, float &y)
 }
 
 // Pairs of every 8 whose exponential runs on the FMA pipe: the other pipe makes four a clock and SM quarter, which
-// alone would take as long as the tensor cores take for the tile.
+// alone would take as long as the tensor cores take for the tile.  (The long prompt: 507 us with three, 566 with none.
+// A cache's loaders need that pipe themselves: 236 us with none, 241 with two.)
 constexpr int kPoly = 3;
 
 // byte offset of 16-byte vector `vec` of row `row` in a [rows][64 channels] block, 128-byte swizzle

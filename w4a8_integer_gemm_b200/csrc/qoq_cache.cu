@@ -17,7 +17,8 @@
 // a rotation followed by a write.  So it is computed in FP32 with a bound on
 // its error, and again in FP64 only where the bound reaches a boundary: the
 // same bits as FP64 throughout, without its four conversions per pair, which
-// a quarter-rate pipe does (they alone took XXX).
+// a quarter-rate pipe does (an append of 12000 tokens, 48 heads:
+// 72 us against 154).
 //
 // Likewise the quantiser multiplies by the reciprocal of the scale, and takes
 // the IEEE division only next to a rounding boundary.
@@ -146,7 +147,7 @@ __device__ __forceinline__ float turn_bound(float amplitude)
 
 // ---------------------------------------------------------------- rotary --
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const uint16_t *__restrict__ x, int64_t ldx,
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const uint16_t *x, int64_t ldx,
                                                           const int32_t *__restrict__ pos, AttnRotary r, int T, int H,
                                                           int d, int tb, uint16_t *y, int64_t ldy)
 {
@@ -359,7 +360,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(AttnCache c, AttnB
     }
 }
 
-// Tokens per CTA: several once the grid fills the GPU anyway.
+// Tokens per CTA: several once the grid fills the GPU anyway.  Appends of 8192 tokens (48 heads) 48 us with four against
+// 59 with one, of 2368 16 against 19, of 1200 13 against 12, of 64 10 against 6.
 int tokens_per_cta(int T)
 {
     return T >= 4 * 148 * kMaxTok ? kMaxTok : 1;
