@@ -74,16 +74,35 @@ int attn_sms();
 // counted in 31 bits.
 int64_t row_tiles(int T, int B, int G, int few);
 bool tiles_fit(int64_t tiles, int Hkv, int table_pages, int page_size);
-// Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows.
+// Launches `kernel` so that it may start as soon as every CTA of the stream's last kernel allows it (early), or after it.
+template <class... P, class... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, bool early, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Row tiles on the tensor cores (qoq_attn_tile.cu) for the sequences with more than `few` rows: the work, or (join) the
+// joining of its parts.  early: the stream's last kernel is the other sequences', beside which the work may run.
 size_t tiles_workspace(int d);
 cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                const AttnBatch &a, int few, float scale, uint16_t *out, int64_t ldo, void *workspace,
-                               cudaStream_t stream);
-// Few rows (qoq_attn_rows.cu): the sequences with at most `few` rows, 8 rows (eight) or 16 to a pass over the cache.
+                               cudaStream_t stream, bool early, bool join);
+// Few rows (qoq_attn_rows.cu): the sequences with at most `few` rows, 8 rows (eight) or 16 to a pass over the cache; the
+// work, or the joining of its parts.
 size_t rows_workspace(int d);
 cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                               const AttnBatch &a, int few, bool eight, float scale, uint16_t *out, int64_t ldo,
-                              void *workspace, cudaStream_t stream);
+                              void *workspace, cudaStream_t stream, bool join);
 // The tile kernel's error flag (a bounded wait ran out), read and cleared.
 cudaError_t read_and_clear_tile_error(int *value);
 cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,

@@ -706,13 +706,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
     }
 }
 
-// Joins the runs that span warps: CTA x the run that ended in warp x's share,
-// one row per warp.  The lanes weigh 32 parts at a time; then the warp adds
-// those that are not empty, in order, a lane holding four channels.
+// Joins the runs that span warps: CTA x the run that ended in warp x's share, one row per warp.  The lanes weigh 128
+// parts at a time, the parts that are not empty go into a list, and the warp adds those, in order, eight loads at a time
+// (a chain of loads is all that this kernel is), a lane holding four channels.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs p)
 {
-    constexpr int kRows = 8 * NT, kStride = D + 4;
+    constexpr int kRows = 8 * NT, kStride = D + 4, kParts = 128, kAhead = 8;
+    __shared__ int s_part[kWarps][kParts];
+    __shared__ float s_f[kWarps][kParts];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     const int last = blockIdx.x;
@@ -724,33 +726,54 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs
         auto part = [&](int w) { return parts + ((size_t)w * 2 + (w == j.w ? 1 : 0)) * kRows * kStride; };
         float M = -INFINITY, L = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w0 = j.w; w0 <= last; w0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (w0 + lane <= last) ml = *reinterpret_cast<const float2 *>(part(w0 + lane) + D);
-            const float m1 = fmaxf(M, warp_max(ml.x));
+        for (int w0 = j.w; w0 <= last; w0 += kParts) {
+            float2 ml[kParts / 32];
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kParts / 32; ++k) {
+                const int w = w0 + 32 * k + lane;
+                ml[k] = w <= last ? *reinterpret_cast<const float2 *>(part(w) + D) : make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < kParts / 32; ++k) top = fmaxf(top, ml[k].x);
+            const float m1 = fmaxf(M, warp_max(top));
             if (m1 == -INFINITY) continue;
             const float f0 = M == -INFINITY ? 0.0f : exp2_fast(M - m1);
-            const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m1);
-            float l = ml.y * f;
+            float l = 0.0f;
+            int count = 0;
+            __syncwarp();                                    // the list has been read
+#pragma unroll
+            for (int k = 0; k < kParts / 32; ++k) {
+                const float f = ml[k].x == -INFINITY ? 0.0f : exp2_fast(ml[k].x - m1);
+                l += ml[k].y * f;
+                const uint32_t some = __ballot_sync(0xffffffffu, f > 0.0f);
+                if (f > 0.0f) {
+                    const int at = count + __popc(some & ((1u << lane) - 1));
+                    s_part[warp][at] = w0 + 32 * k + lane;
+                    s_f[warp][at] = f;
+                }
+                count += __popc(some);
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             M = m1;
             L = fmaf(L, f0, l);
             v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-            uint32_t todo = __ballot_sync(0xffffffffu, f > 0.0f);
-            while (todo) {
-                float4 y[4];
-                float g[4];
+            __syncwarp();
+            for (int i = 0; i < count; i += kAhead) {
+                float4 y[kAhead];
+                float g[kAhead];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = todo ? __ffs(todo) - 1 : 0;
-                    g[u] = todo ? __shfl_sync(0xffffffffu, f, i) : 0.0f;
+                for (int u = 0; u < kAhead; ++u) {
+                    g[u] = 0.0f;
                     y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (todo && lane < D / 4) y[u] = reinterpret_cast<const float4 *>(part(w0 + i))[lane];
-                    todo &= todo - 1;
+                    if (i + u < count) {
+                        g[u] = s_f[warp][i + u];
+                        if (lane < D / 4) y[u] = reinterpret_cast<const float4 *>(part(s_part[warp][i + u]))[lane];
+                    }
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < kAhead; ++u)
                     v = make_float4(fmaf(y[u].x, g[u], v.x), fmaf(y[u].y, g[u], v.y), fmaf(y[u].z, g[u], v.z),
                                     fmaf(y[u].w, g[u], v.w));
             }
@@ -767,27 +790,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs
 constexpr int kMaxCtas = 2 * 160;       // sizes the workspace: two CTAs per SM
 
 template <int D, int BITS, int NT>
-cudaError_t launch_rows(RowsArgs p, cudaStream_t stream)
+cudaError_t launch_rows(const RowsArgs &p, cudaStream_t stream, bool join)
 {
     const int ctas = min(attn_sms() * (NT == 1 ? 2 : 1), NT == 1 ? kMaxCtas : kMaxCtas / 2);
+    // (the join's CTAs come up as the others end, and wait for the last)
+    if (join) return launch_kernel(attn_rows_join_kernel<D, NT>, dim3(ctas * kWarps), kThreads, 0, stream, true, p);
     constexpr int smem = RowsCfg<D, BITS, NT>::kSmem;
-    auto kernel = attn_rows_kernel<D, BITS, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, kThreads, smem, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // the join's CTAs come up while the first kernel runs and wait for its end
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas * kWarps);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<D, NT>, p);
+    return launch_kernel(attn_rows_kernel<D, BITS, NT>, dim3(ctas), kThreads, smem, stream, false, p);
 }
 
 }  // namespace
@@ -800,17 +811,17 @@ size_t rows_workspace(int d)
 
 cudaError_t launch_paged_rows(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                               const AttnBatch &a, int few, bool eight, float scale, uint16_t *out, int64_t ldo,
-                              void *workspace, cudaStream_t stream)
+                              void *workspace, cudaStream_t stream, bool join)
 {
     int4 *joined = reinterpret_cast<int4 *>(workspace);
     RowsArgs p{q, ldq, ldo, out, c, a, T, Hq, Hkv, Hq / Hkv, few, scale * 1.4426950408889634f, 0x64006400u, 0x54005400u,
                reinterpret_cast<float *>(joined + kMaxCtas * kWarps), joined};
     if (d == 128) {
-        if (c.bits == 4) return eight ? launch_rows<128, 4, 1>(p, stream) : launch_rows<128, 4, 2>(p, stream);
-        return eight ? launch_rows<128, 8, 1>(p, stream) : launch_rows<128, 8, 2>(p, stream);
+        if (c.bits == 4) return eight ? launch_rows<128, 4, 1>(p, stream, join) : launch_rows<128, 4, 2>(p, stream, join);
+        return eight ? launch_rows<128, 8, 1>(p, stream, join) : launch_rows<128, 8, 2>(p, stream, join);
     }
-    if (c.bits == 4) return eight ? launch_rows<64, 4, 1>(p, stream) : launch_rows<64, 4, 2>(p, stream);
-    return eight ? launch_rows<64, 8, 1>(p, stream) : launch_rows<64, 8, 2>(p, stream);
+    if (c.bits == 4) return eight ? launch_rows<64, 4, 1>(p, stream, join) : launch_rows<64, 4, 2>(p, stream, join);
+    return eight ? launch_rows<64, 8, 1>(p, stream, join) : launch_rows<64, 8, 2>(p, stream, join);
 }
 
 }  // namespace qoq

@@ -31,7 +31,7 @@
 // shares, one per CTA; an item that spans CTAs leaves a part in each, and a
 // second kernel joins them.  (Whole items, and keys cut into equal numbers of
 // tiles per item: chunks of 450 to 600 tokens over up to 13600 255 us against
-// 235, a mixed batch of short chunks 94 us against 75.)
+// 235, a mixed batch of short chunks 94 us against 76.)
 //
 // Bound: for each row tile a step is a chain, softmax (about 1300 cycles of
 // its 16 warps' exponentials and conversions, 900 of waits and stores) and
@@ -894,7 +894,12 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     }
     tc_fence_before();
     __syncthreads();
-    if (BITS) grid_launch_dependents();
+    if (BITS) {
+        grid_launch_dependents();
+        // This grid may run beside the one before it, and does not need its results; but whoever waits for this one
+        // waits for both.
+        grid_dependency_wait();
+    }
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
     if (threadIdx.x == 0 && abort_flag) atomicExch(&g_tile_error, 1);
 }
@@ -917,15 +922,29 @@ __global__ void __launch_bounds__(kJoinRows *D / 4) attn_tile_join_kernel(const 
     if (row >= n * G - j.y) return;
     float M = -INFINITY, L = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = j.w; c <= last; ++c) {
-        const float *src = part + ((size_t)c * 2 + (c == j.w ? 1 : 0)) * kRows * (D + 2);
-        const float2 ml = reinterpret_cast<const float2 *>(src + kRows * D)[row];
-        const float4 x = reinterpret_cast<const float4 *>(src)[at * kRows + row];
-        if (ml.y <= 0.0f) continue;                  // saw nothing, and wrote no sums
-        const float m1 = fmaxf(M, ml.x), f0 = M == -INFINITY ? 0.0f : ex2(M - m1), f1 = ex2(ml.x - m1);
-        M = m1;
-        L = fmaf(L, f0, ml.y * f1);
-        v = make_float4(fmaf(v.x, f0, x.x * f1), fmaf(v.y, f0, x.y * f1), fmaf(v.z, f0, x.z * f1), fmaf(v.w, f0, x.w * f1));
+    constexpr int kAhead = 4;                        // parts loaded at a time
+    for (int c0 = j.w; c0 <= last; c0 += kAhead) {
+        float2 ml[kAhead];
+        float4 x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + u;
+            ml[u] = make_float2(0.0f, 0.0f);
+            if (c <= last) {
+                const float *src = part + ((size_t)c * 2 + (c == j.w ? 1 : 0)) * kRows * (D + 2);
+                ml[u] = reinterpret_cast<const float2 *>(src + kRows * D)[row];
+                x[u] = reinterpret_cast<const float4 *>(src)[at * kRows + row];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (ml[u].y <= 0.0f) continue;           // saw nothing, and wrote no sums
+            const float m1 = fmaxf(M, ml[u].x), f0 = M == -INFINITY ? 0.0f : ex2(M - m1), f1 = ex2(ml[u].x - m1);
+            M = m1;
+            L = fmaf(L, f0, ml[u].y * f1);
+            v = make_float4(fmaf(v.x, f0, x[u].x * f1), fmaf(v.y, f0, x[u].y * f1), fmaf(v.z, f0, x[u].z * f1),
+                            fmaf(v.w, f0, x[u].w * f1));
+        }
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const int r = j.y + row;
@@ -937,30 +956,18 @@ __global__ void __launch_bounds__(kJoinRows *D / 4) attn_tile_join_kernel(const 
 constexpr int kMaxTileCtas = 160;       // sizes the workspace
 
 template <int D, int BITS>
-cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream)
+cudaError_t launch_tile(const TileArgs &p, cudaStream_t stream, bool early, bool join)
 {
-    auto kernel = attn_tile_kernel<D, BITS>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
-    if (e != cudaSuccess) return e;
     // one CTA per SM (shared and tensor memory allow no more), each with its share of the work
     const int64_t items = BITS ? row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv * 64 : row_tiles(p.T, p.a.B, p.G, p.few) * p.Hkv;
     const int ctas = (int)std::min<int64_t>(items, std::min(attn_sms(), kMaxTileCtas));
-    kernel<<<ctas, tile_threads(BITS), TileCfg<D>::kSmem, stream>>>(p);
-    if (BITS == 0) return cudaGetLastError();
-    const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return e1;
-    // the join's CTAs come up as the others end, and wait for the last
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, kRows / kJoinRows);
-    cfg.blockDim = dim3(kJoinRows * D / 4);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tile_join_kernel<D>, (const float *)p.part, (const int4 *)p.joined, p.a, p.Hkv, p.G,
-                              p.out, p.ldo);
+    if (join)
+        return launch_kernel(attn_tile_join_kernel<D>, dim3(ctas, kRows / kJoinRows), kJoinRows * D / 4, 0, stream, true,
+                             (const float *)p.part, (const int4 *)p.joined, p.a, p.Hkv, p.G, p.out, p.ldo);
+    auto kernel = attn_tile_kernel<D, BITS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, dim3(ctas), tile_threads(BITS), TileCfg<D>::kSmem, stream, early, p);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1026,7 +1033,7 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
     cudaError_t e = encode_rows(&p.map_k, k, T, Hkv * d, ldk);
     if (e == cudaSuccess) e = encode_rows(&p.map_v, v, T, Hkv * d, ldv);
     if (e != cudaSuccess) return e;
-    return d == 128 ? launch_tile<128, 0>(p, stream) : launch_tile<64, 0>(p, stream);
+    return d == 128 ? launch_tile<128, 0>(p, stream, false, false) : launch_tile<64, 0>(p, stream, false, false);
 }
 
 size_t tiles_workspace(int d)
@@ -1041,14 +1048,14 @@ bool tiles_fit(int64_t tiles, int Hkv, int table_pages, int page_size)
 
 cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, int Hkv, int d, const AttnCache &c,
                                const AttnBatch &a, int few, float scale, uint16_t *out, int64_t ldo, void *workspace,
-                               cudaStream_t stream)
+                               cudaStream_t stream, bool early, bool join)
 {
     int4 *joined = reinterpret_cast<int4 *>(workspace);
     TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, reinterpret_cast<float *>(joined + kMaxTileCtas), joined, c, a, T, Hq,
                Hkv, Hq / Hkv, few, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
-    if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream) : launch_tile<128, 8>(p, stream);
-    return c.bits == 4 ? launch_tile<64, 4>(p, stream) : launch_tile<64, 8>(p, stream);
+    if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream, early, join) : launch_tile<128, 8>(p, stream, early, join);
+    return c.bits == 4 ? launch_tile<64, 4>(p, stream, early, join) : launch_tile<64, 8>(p, stream, early, join);
 }
 
 cudaError_t read_and_clear_tile_error(int *value)
