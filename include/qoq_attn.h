@@ -32,6 +32,8 @@
  *   - T, B == 0 are valid empty problems: QOQ_OK, nothing launched.
  *   - Index arrays are read on the device and checked there: an index that
  *     points outside its array skips the access, as said below.
+ *   - Waits inside the kernels are bounded; one that runs out is reported by
+ *     qoq_device_error, and the call's outputs are then unspecified.
  *
  * One description of a batch serves every call:
  *   cu      int32 [B + 1]  sequence b's new tokens are rows cu[b] ..

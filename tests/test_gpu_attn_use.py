@@ -274,6 +274,97 @@ def test_strides_of_eight(extra):
         assert bool((w[:, :8] == 7).all()) and bool((w[:, 8 + Hq * d:] == 7).all())
 
 
+@pytest.mark.parametrize("G,Hkv,new,d,bits", [(17, 2, [1, 1], 64, 4), (32, 1, [1, 1, 1], 128, 8), (33, 1, [1, 1], 128, 4), (20, 1, [2, 1], 64, 8),
+                                             (11, 1, [3, 2, 1], 128, 4), (8, 2, [4, 5, 1], 64, 4)])
+def test_rows_either_kernel_takes(G, Hkv, new, d, bits):
+    """Numbers of rows on both sides of every choice of kernel: 8, 16, 32 and more per KV head."""
+    b = Batch(new, [300 + 40 * i for i in range(len(new))], 16, seed=G)
+    c = _filled_pool(b, Hkv, d, bits, seed=1)
+    Q = _half(_rng(G), b.T, G * Hkv, d)
+    for most in (None, max(new), 1):
+        o = q.qattn_paged_attention(_dev(Q), c, *b.dev, max_new=most)
+        _check_paged(b, c, Q, Hkv, bits, d ** -0.5, o.cpu().numpy())
+
+
+@pytest.mark.parametrize("new", [[1, 2], [90, 1]])
+def test_rows_before_the_first_sequence(new):
+    """cu begins after rows of no sequence: they are neither read nor written, by any call."""
+    d, Hq, Hkv, bits, lead, tail = 64, 4, 2, 4, 3, 2
+    b = Batch(new, [n + 20 for n in new], 16, seed=1)
+    c = _filled_pool(b, Hkv, d, bits, seed=2)
+    x = _half(_rng(3), lead + b.T + tail, Hq + 2 * Hkv, d)
+    xd = _dev(x)
+    inner = xd[lead:lead + b.T].clone()
+    xd[:lead] = float("nan")
+    xd[lead + b.T:] = float("nan")
+    cu = b.dev[1] + lead
+    rotary = q.Rotary(_dev(_freq(d)))
+
+    def run(y, cu, c):
+        qh, kh, vh = y.split([Hq, Hkv, Hkv], 1)
+        outs = [torch.full((y.shape[0], h, d), 7.0, dtype=torch.float16, device=DEV) for h in (Hq, Hkv, Hkv, Hq, Hq)]
+        q.qattn_cache_append(kh, vh, c, b.dev[0], cu, b.dev[2], rotary=rotary, q=qh, q_out=outs[0])
+        q.qattn_cache_read(c, b.dev[0], cu, b.dev[2], y.shape[0], K=outs[1], V=outs[2])
+        q.qattn_paged_attention(outs[0], c, b.dev[0], cu, b.dev[2], out=outs[3])
+        q.qattn_prompt_attention(qh, kh, vh, cu, out=outs[4])
+        return outs
+
+    c2 = _filled_pool(b, Hkv, d, bits, seed=2)
+    for got, want in zip(run(xd, cu, c), run(inner, b.dev[1], c2)):
+        assert bool((got[:lead] == 7).all()) and bool((got[lead + b.T:] == 7).all())
+        assert torch.equal(_bits(got[lead:lead + b.T]), _bits(want))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3], [200, 150]])
+def test_lengths_beyond_the_table(new):
+    """Contexts longer than their row of the table: what the table does not reach is not there."""
+    d, Hq, Hkv, bits, page = 128, 4, 2, 8, 16
+    b = Batch(new, [500, 333], page, seed=1)
+    c = _filled_pool(b, Hkv, d, bits, seed=2)
+    b.table = np.ascontiguousarray(b.table[:, :13])           # 208 tokens, the middle of a key tile
+    b.dev = (_dev(b.table), *b.dev[1:])
+    x = _half(_rng(3), b.T, Hq + 2 * Hkv, d)
+    qh, kh, vh = _dev(x).split([Hq, Hkv, Hkv], 1)
+    q.qattn_cache_append(kh, vh, c, *b.dev)
+    for most in (max(new), 1):
+        o = q.qattn_paged_attention(qh, c, *b.dev, max_new=most)
+        _check_paged(b, c, x[:, :Hq], Hkv, bits, d ** -0.5, o.cpu().numpy())
+    K, V = q.qattn_cache_read(c, *b.dev, b.T)
+    gone = _dev(b.pos >= 208)
+    assert bool((K[gone] == 0).all()) and bool((V[gone] == 0).all())
+
+
+def test_append_in_place():
+    d, Hq, Hkv = 128, 5, 1
+    b = Batch([3, 70], [30, 70], 32, seed=1)
+    x = _dev(_half(_rng(3), b.T, Hq + 2 * Hkv, d))
+    rotary = q.Rotary(_dev(_freq(64)), True, 1.1)
+    pools = [_poisoned_pool(b, Hkv, d, 4) for _ in range(2)]
+    qh, kh, vh = x.split([Hq, Hkv, Hkv], 1)
+    want = q.qattn_cache_append(kh, vh, pools[0], *b.dev, rotary=rotary, q=qh)
+    assert q.qattn_cache_append(kh, vh, pools[1], *b.dev, rotary=rotary, q=qh, q_out=qh) is qh
+    assert torch.equal(_bits(qh), _bits(want))
+    for s, t in zip((pools[0].k_codes, pools[0].v_codes, pools[0].k_par, pools[0].v_par),
+                    (pools[1].k_codes, pools[1].v_codes, pools[1].k_par, pools[1].v_par)):
+        assert torch.equal(s.view(torch.uint8), t.view(torch.uint8))
+
+
+def test_negative_lengths_and_empty_contexts():
+    """Lengths of zero and below: every row sees nothing and is zero, whichever kernel has it."""
+    d, Hq, Hkv = 64, 4, 1
+    b = Batch([1, 40, 2, 3], [5, 60, 9, 300], 16, seed=1)
+    c = _filled_pool(b, Hkv, d, 4, seed=2)
+    kl = _dev(np.array([0, -5, -(1 << 31), 300], dtype=np.int32))
+    Q = _half(_rng(1), b.T, Hq, d)
+    b.kv = [0, -5, -5, 300]
+    for most in (40, 1):
+        o = q.qattn_paged_attention(_dev(Q), c, b.dev[0], b.dev[1], kl, max_new=most).cpu().numpy()
+        assert not o[:43].any()
+        one = Batch([3], [300], 16)
+        one.table, one.pages, one.cu, one.pos = b.table[3:], b.pages, one.cu, b.pos[43:]
+        _check_paged(one, c, Q[43:], Hkv, 4, d ** -0.5, o[43:])
+
+
 def test_empty_calls():
     d, Hq, Hkv = 64, 4, 2
     c = q.paged_kv_cache(3, Hkv, d)

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             else hi = mid - 1;
         }
         long long skip = at - s_before[lo];
-        for (run.b = lo * per;; ++run.b) {
+        for (run.b = lo * per; run.b < a.B; ++run.b) {
             const long long len = length_of(run.b, run.n, run.grains);
             if (skip < len) break;
             skip -= len;
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         run.hk = r % p.Hkv;
         run.row0 = r / p.Hkv * C::kRows;
         at -= skip % unit;                           // where the run begins; the share begins (`from`) within it
+        if (run.b >= a.B) end = at;                  // (the sums ran over: rows counted in several sequences)
         }
     }
     uint8_t *ring_ptr = smem + warp * C::kStages * C::kStage;
@@ -672,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     run.row0 = 0;
                     do {
                         ++run.b;
-                    } while (length_of(run.b, run.n, run.grains) == 0);
+                    } while (run.b < a.B && length_of(run.b, run.n, run.grains) == 0);
+                    if (run.b >= a.B) break;         // (the sums ran over: rows counted in several sequences)
                 }
             }
         }

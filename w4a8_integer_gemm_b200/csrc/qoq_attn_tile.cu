@@ -511,11 +511,12 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     w.slot = -1;
                     w.j0 = w.first = 0;
                     int tile = x / p.Hkv, count;
-                    for (w.b = misc.chunk[chunk_at(tile)] * per_chunk;; ++w.b) {
+                    for (w.b = misc.chunk[chunk_at(tile)] * per_chunk; w.b < p.a.B; ++w.b) {
                         count = tiles_of(w.b, w.n);
                         if (tile < count) break;
                         tile -= count;
                     }
+                    if (w.b >= p.a.B) break;                 // (the sums ran over: rows counted in several sequences)
                     w.row0 = (count - 1 - tile) * kRows;
                     ok = emit(1 << 30);
                 }
@@ -530,8 +531,10 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     int x = at, lo = chunk_at(x), units = 0;
                     int in_chunk = 0;
                     // the first row tile: x becomes the place in it
-                    for (bool found = false; !found;) {
+                    bool found = false;
+                    while (!found) {
                         w.b = misc.chunk[lo] * per_chunk + in_chunk;
+                        if (w.b >= p.a.B) break;             // (the sums ran over: rows counted in several sequences)
                         const int tiles = tiles_of(w.b, w.n);
                         w.first = first_of(w.b, w.n);
                         for (w.row0 = (tiles - 1) * kRows; w.row0 >= 0; w.row0 -= kRows) {
@@ -542,9 +545,9 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         }
                         if (!found) ++in_chunk;
                     }
-                    w.hk = x / units;
-                    w.j0 = x % units;
-                    while (ok) {
+                    w.hk = found ? x / units : 0;
+                    w.j0 = found ? x % units : 0;
+                    while (ok && found) {
                         const int j1 = min(units, w.j0 + end - at);
                         w.slot = w.j0 == 0 && j1 == units ? -1 : w.j0 == 0 ? 1 : 0;
                         if (w.slot == 0 && j1 == units && lane == 0)
@@ -560,13 +563,14 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         while (w.row0 < 0) {                 // the next sequence with tiles
                             if (++in_chunk == per_chunk || misc.chunk[lo] * per_chunk + in_chunk >= p.a.B) {
                                 in_chunk = 0;
-                                ++lo;
+                                found = ++lo < kChunks;
+                                if (!found) break;
                             }
                             w.b = misc.chunk[lo] * per_chunk + in_chunk;
                             w.row0 = w.b < p.a.B ? (tiles_of(w.b, w.n) - 1) * kRows : -1;
                             w.first = w.b < p.a.B ? first_of(w.b, w.n) : 0;
                         }
-                        units = units_of(w.first, w.n, w.row0);
+                        if (found) units = units_of(w.first, w.n, w.row0);
                     }
                 }
             }
