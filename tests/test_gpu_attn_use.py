@@ -240,6 +240,35 @@ def test_many_sequences():
         _check_prompt(x[e], [lens[s]], Hq, Hkv, p[e], d ** -0.5)
 
 
+@pytest.mark.parametrize("G,d,bits", [(4, 128, 4), (3, 128, 8), (1, 64, 8), (16, 64, 4)])
+def test_many_work_items(G, d, bits):
+    """Hundreds of short chunks and prompts: every SM gets many row tiles one after another."""
+    Hkv, B = 8, 170
+    r = _rng(G)
+    new = [int(n) for n in r.integers(1, 2 + 200 // G, B)]
+    kv = [n + int(k) for n, k in zip(new, r.integers(0, 150, B))]
+    b = Batch(new, kv, 32, seed=2)
+    c = _filled_pool(b, Hkv, d, bits, seed=3)
+    x = _half(r, b.T, (G + 2) * Hkv, d)
+    qh, kh, vh = _dev(x).split([G * Hkv, Hkv, Hkv], 1)
+    o = q.qattn_paged_attention(qh, c, *b.dev)
+    p = q.qattn_prompt_attention(qh, kh, vh, b.dev[1]).cpu().numpy()
+    torch.cuda.synchronize()
+    assert q.qoq_device_error() == q.QOQ_OK
+    some = list(range(0, B, 23))
+    rows = np.concatenate([np.arange(b.cu[s], b.cu[s + 1]) for s in some])
+    _check_paged(b, c, x[:, :G * Hkv], Hkv, bits, d ** -0.5, o.cpu().numpy(), rows=rows)
+    for s in some:
+        e = slice(b.cu[s], b.cu[s + 1])
+        _check_prompt(x[e], [new[s]], G * Hkv, Hkv, p[e], d ** -0.5)
+    # the others against themselves: a sequence's outputs do not depend on its place in the batch
+    turn = np.arange(B)[::-1]
+    back = Batch([new[i] for i in turn], [kv[i] for i in turn], 32, seed=2)
+    order = np.concatenate([np.arange(b.cu[i], b.cu[i + 1]) for i in turn])
+    again = q.qattn_prompt_attention(*(y[_dev(order)] for y in (qh, kh, vh)), back.dev[1]).cpu().numpy()
+    assert np.array_equal(again.view(np.int16), p[order].view(np.int16))
+
+
 @pytest.mark.parametrize("extra", [8, 24])
 def test_strides_of_eight(extra):
     """Rows whose distance is a multiple of 16 bytes and no more, in every argument."""

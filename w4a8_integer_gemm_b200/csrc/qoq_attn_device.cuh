@@ -54,20 +54,6 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, volati
     return true;
 }
 
-// The 8 channels of a 16-byte vector in the order the 4-bit codes expand to:
-// 0 4 1 5 2 6 3 7 (the two halves of a code word give a pair).
-__device__ __forceinline__ uint4 to_code_order(uint4 v)
-{
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                      __byte_perm(v.y, v.w, 0x7632));
-}
-
-__device__ __forceinline__ uint4 from_code_order(uint4 v)
-{
-    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                      __byte_perm(v.z, v.w, 0x7632));
-}
-
 __device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -102,21 +88,20 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 x)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 
-// Eight 4-bit codes -> fp16(s c + m) of channels 0 4, 1 5, 2 6, 3 7.  A
-// nibble in bits 0-3 under the exponent of 1024 is 1024 + c, in bits 4-7
-// under that of 64 it is 64 + c (the mantissa's unit is 2^-4 there): one
-// logic operation and one exact subtraction give c, one multiply-add rounds
-// once.  par: (s, m).  The exponent patterns e6 = 0x64006400 and e5 =
-// 0x54005400 come in registers whose values the compiler does not know: a
+// Eight 4-bit codes -> fp16(s c + m), in order.  A nibble in bits 0-3 under
+// the exponent of 1024 is 1024 + c, in bits 4-7 under that of 64 it is
+// 64 + c (the mantissa's unit is 2^-4 there); so with a byte in both halves of
+// a word one logic operation and one exact subtraction give its two codes,
+// and one multiply-add rounds once.  par: (s, m).  The exponent patterns come
+// in a register, e4 = 0x54006400, whose value the compiler does not know: a
 // logic instruction has room for one constant, and with two it becomes two.
-__device__ __forceinline__ uint4 expand4(uint32_t x, uint32_t par, uint32_t e6, uint32_t e5)
+__device__ __forceinline__ uint4 expand4(uint32_t x, uint32_t par, uint32_t e4)
 {
     const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
-    const uint32_t y = x >> 8;
-    const uint32_t a = sub_h2((x & 0x000F000Fu) | e6, 0x64006400u);
-    const uint32_t b = sub_h2((x & 0x00F000F0u) | e5, 0x54005400u);
-    const uint32_t c = sub_h2((y & 0x000F000Fu) | e6, 0x64006400u);
-    const uint32_t d = sub_h2((y & 0x00F000F0u) | e5, 0x54005400u);
+    const uint32_t a = sub_h2((__byte_perm(x, x, 0x0000) & 0x00F0000Fu) | e4, 0x54006400u);
+    const uint32_t b = sub_h2((__byte_perm(x, x, 0x1111) & 0x00F0000Fu) | e4, 0x54006400u);
+    const uint32_t c = sub_h2((__byte_perm(x, x, 0x2222) & 0x00F0000Fu) | e4, 0x54006400u);
+    const uint32_t d = sub_h2((__byte_perm(x, x, 0x3333) & 0x00F0000Fu) | e4, 0x54006400u);
     return make_uint4(fma_h2(a, s, m), fma_h2(b, s, m), fma_h2(c, s, m), fma_h2(d, s, m));
 }
 

@@ -21,7 +21,8 @@
 //   MMA              S = Q K^T (both from shared memory), O += P V (P from
 //                    tensor memory, V with its channels contiguous).
 //   Q                the next item's Q as soon as the last S of this one is
-//                    done.
+//                    done.  (Boxes by TMA, where the group's heads divide
+//                    128, were no faster: the softmax is not done earlier.)
 //   plan             the list, a few items ahead, in a ring of descriptions.
 // Tensor memory: S0 S1 (128 columns each, P over the first half), O0 O1 (D
 // columns each).
@@ -31,7 +32,7 @@
 // shares, one per CTA; an item that spans CTAs leaves a part in each, and a
 // second kernel joins them.  (Whole items, and keys cut into equal numbers of
 // tiles per item: chunks of 450 to 600 tokens over up to 13600 255 us against
-// 235, a mixed batch of short chunks 94 us against 76.)
+// 235, a mixed batch of short chunks 94 us against 76, at that time.)
 //
 // Bound: for each row tile a step is a chain, softmax (about 1300 cycles of
 // its 16 warps' exponentials and conversions, 900 of waits and stores) and
@@ -119,7 +120,7 @@ struct TileArgs {
     int few;                // sequences with at most this many rows (n_b * G) are another kernel's
     float scale_log2;       // |scale| * log2(e)
     uint32_t flip;          // 0x80008000 when scale < 0: the sign goes into q
-    uint32_t e6, e5;        // 0x64006400, 0x54005400 (expand4)
+    uint32_t e6, e4;        // 0x64006400, 0x54006400 (expand8, expand4)
     bool wide;              // out's rows begin on 32-byte boundaries: half as many store instructions, which the
                             // load/store unit takes line by line (packed prompts 153 us against 165)
     CUtensorMap map_k, map_v;   // (prompts) [T][Hkv * D], boxes of 64 channels x 128 rows, 128-byte swizzle
@@ -204,7 +205,7 @@ __device__ __forceinline__ void regs_down()
 // Registers per thread of the roles; a block of 640 threads is launched with 96 of them for each, one of 768 with 80.
 template <int BITS>
 struct Regs {
-    static constexpr int kSoftmax = BITS ? 96 : 104, kLoader = BITS ? 56 : 0, kRest = BITS ? 40 : 64;
+    static constexpr int kSoftmax = BITS ? 96 : 104, kLoader = BITS ? 48 : 0, kRest = BITS ? 48 : 64;
     static_assert(512 * kSoftmax + (BITS ? 128 * kLoader : 0) + 128 * kRest <= tile_threads(BITS) * (BITS ? 80 : 96), "register split");
 };
 
@@ -444,14 +445,13 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
-                if (BITS == 4 || p.flip) {                   // each lane its own vectors
+                if (p.flip) {                                // each lane its own vectors
 #pragma unroll 2
                     for (int r = r0; r < kRows; r += kPass) {
                         const uint32_t off = offset(r - r0 % 8) - offset(r0 - r0 % 8);
 #pragma unroll
                         for (int j = 0; j < kN; ++j) {
-                            uint4 x = ld_shared16(at[j] + off);
-                            if (BITS == 4) x = to_code_order(x);
+                            const uint4 x = ld_shared16(at[j] + off);
                             st_shared16(at[j] + off, make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip));
                         }
                     }
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     for (int u = 0; u < kVecs; ++u) {
                         constexpr int kHalf = kVecs / 2;
                         uint4 x;
-                        if (kB == 4) x = expand4(twist ? cw[u ^ kHalf] : cw[u], pr[i], p.e6, p.e5);
+                        if (kB == 4) x = expand4(twist ? cw[u ^ kHalf] : cw[u], pr[i], p.e4);
                         else x = expand8(twist ? cw[2 * (u ^ kHalf) % 4] : cw[2 * u % 4],
                                          twist ? cw[(2 * (u ^ kHalf) + 1) % 4] : cw[(2 * u + 1) % 4], pr[i], p.e6);
                         // (a batch's rows are a multiple of 8 from the first batch's: the same swizzle)
@@ -857,11 +857,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                         const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
                         y[u] = l > 0.0f ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
                     }
-                    uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-                    if (BITS == 4) {
-                        a = from_code_order(a);
-                        b = from_code_order(b);
-                    }
+                    const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
                     if (real) {
                         if (p.wide) {
                             st_global32(dst + c, a, b);
@@ -882,11 +878,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     if (real && l > 0.0f) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const uint32_t *x = o + 8 * (u >> 1);
-                            // columns 8v .. 8v + 7 hold channels 0 4 1 5 2 6 3 7 of a 4-bit cache
-                            uint4 y = make_uint4(x[4 * (u & 1)], x[4 * (u & 1) + 1], x[4 * (u & 1) + 2], x[4 * (u & 1) + 3]);
-                            if (BITS == 4) y = make_uint4(x[u & 1], x[2 + (u & 1)], x[4 + (u & 1)], x[6 + (u & 1)]);
-                            reinterpret_cast<uint4 *>(dst)[(c / 4 + u) * kRows] = y;
+                            reinterpret_cast<uint4 *>(dst)[(c / 4 + u) * kRows] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
                         }
                     }
                 }
@@ -1032,7 +1024,7 @@ cudaError_t launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16
                                     int64_t ldv, int T, int Hq, int Hkv, int d, const AttnBatch &a, float scale,
                                     uint16_t *out, int64_t ldo, cudaStream_t stream)
 {
-    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 0, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
+    TileArgs p{q, k, v, ldq, ldk, ldv, ldo, out, nullptr, nullptr, AttnCache{}, a, T, Hq, Hkv, Hq / Hkv, 0, 0.0f, 0u, 0x64006400u, 0x54006400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
     cudaError_t e = encode_rows(&p.map_k, k, T, Hkv * d, ldk);
     if (e == cudaSuccess) e = encode_rows(&p.map_v, v, T, Hkv * d, ldv);
@@ -1056,7 +1048,7 @@ cudaError_t launch_paged_tiles(const uint16_t *q, int64_t ldq, int T, int Hq, in
 {
     int4 *joined = reinterpret_cast<int4 *>(workspace);
     TileArgs p{q, nullptr, nullptr, ldq, 0, 0, ldo, out, reinterpret_cast<float *>(joined + kMaxTileCtas), joined, c, a, T, Hq,
-               Hkv, Hq / Hkv, few, 0.0f, 0u, 0x64006400u, 0x54005400u, wide_rows(out, ldo), {}, {}};
+               Hkv, Hq / Hkv, few, 0.0f, 0u, 0x64006400u, 0x54006400u, wide_rows(out, ldo), {}, {}};
     set_scale(p, scale);
     if (d == 128) return c.bits == 4 ? launch_tile<128, 4>(p, stream, early, join) : launch_tile<128, 8>(p, stream, early, join);
     return c.bits == 4 ? launch_tile<64, 4>(p, stream, early, join) : launch_tile<64, 8>(p, stream, early, join);

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(
 // A thread takes kAhead vectors of 8 channels at a time, all their loads before the first use.
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(AttnCache c, AttnBatch a, int T, int Hkv, int tb,
-                                                              uint32_t e6, uint32_t e5, uint16_t *__restrict__ K,
+                                                              uint32_t e6, uint32_t e4, uint16_t *__restrict__ K,
                                                               uint16_t *__restrict__ V)
 {
     constexpr int kVecs = D / 8, kAhead = 4;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(AttnCache c, AttnB
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             // (an absent page: codes and parameters 0, so zeros)
-            if (dst[u]) *dst[u] = BITS == 4 ? from_code_order(expand4(codes[u].x, par[u], e6, e5))
+            if (dst[u]) *dst[u] = BITS == 4 ? expand4(codes[u].x, par[u], e4)
                                             : expand8(codes[u].x, codes[u].y, par[u], e6);
         }
     }
@@ -400,7 +400,7 @@ cudaError_t launch_cache_read(const AttnCache &c, const AttnBatch &a, int T, int
     // eight vectors per thread, as long as that leaves four CTAs per SM
     const int want = 8 * kThreads / (2 * Hkv * (d / 8)), most = T / (4 * 148);
     const int tb = std::max(1, std::min({want, most, kMaxReadTok}));
-    auto run = [&](auto kernel) { kernel<<<(T + tb - 1) / tb, kThreads, 0, stream>>>(c, a, T, Hkv, tb, 0x64006400u, 0x54005400u, K, V); };
+    auto run = [&](auto kernel) { kernel<<<(T + tb - 1) / tb, kThreads, 0, stream>>>(c, a, T, Hkv, tb, 0x64006400u, 0x54006400u, K, V); };
     if (d == 128) c.bits == 4 ? run(cache_read_kernel<128, 4>) : run(cache_read_kernel<128, 8>);
     else c.bits == 4 ? run(cache_read_kernel<64, 4>) : run(cache_read_kernel<64, 8>);
     return cudaGetLastError();
