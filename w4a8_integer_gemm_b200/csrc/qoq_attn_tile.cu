@@ -844,6 +844,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             s_row[t][h][r] = l;
             named_barrier(mates, 64);
             l = s_row[t][0][r] + s_row[t][1][r];
+            named_barrier(mates, 64);       // s_row has been read: the next item, without keys for this row tile, writes it at once
             const int g = real ? (w.row0 + row) % p.G : 0;
             if (BITS == 0 || w.slot < 0) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
