@@ -321,17 +321,23 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
     tc_fence_after();
     const uint32_t tmem = misc.tmem_slot;
     // The next item, from the scheduler's ring; false at the end of the list, or when a wait ran out.  Every role walks
-    // the same list.
+    // the same list.  Warps that meet in barriers take an item together or not at all: get_together().
     int turn = 0;                                    // items read so far
     TileItem w;
-    auto get = [&]() -> bool {
+    auto take = [&](bool there) -> bool {
+        if (!there) return false;
         const int i = turn % kAhead;
-        if (!__all_sync(0xffffffffu, wait_short(ifull(i), (uint32_t)(turn / kAhead) & 1, &abort_flag, kBudgetNs))) return false;
         w = misc.item[i];
         __syncwarp();
         if (lane == 0) mbar_arrive(iempty(i));
         ++turn;
         return w.b >= 0;
+    };
+    auto get = [&]() -> bool {
+        return take(__all_sync(0xffffffffu, wait_short(ifull(turn % kAhead), (uint32_t)(turn / kAhead) & 1, &abort_flag, kBudgetNs)));
+    };
+    auto get_together = [&](int id, int count, bool polls) -> bool {
+        return take(group_wait(id, count, polls, ifull(turn % kAhead), (uint32_t)(turn / kAhead) & 1));
     };
 
     if (BITS ? warp >= 20 : warp >= 16) {
@@ -405,11 +411,10 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
                 base += 2 * w.steps;
             }
-            if (!ok) {      // let what was issued finish before tensor memory is freed
-                mma_commit_lead(lead, done);
-                const uint64_t end = global_timer_ns() + 200000000ull;
-                while (!mbar_try_wait(done, 0) && global_timer_ns() < end) {
-                }
+            // However the list ended, what was issued finishes before tensor memory and the barriers go.
+            mma_commit_lead(lead, done);
+            const uint64_t end = global_timer_ns() + 200000000ull;
+            while (!mbar_try_wait(done, 0) && global_timer_ns() < end) {
             }
         }
         if (warp >= kQWarp && warp < kQWarp + kQWarps) {
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                 }
             }
-            if (!ok && lane == 0) {     // let the copies in flight land before the shared memory goes away
+            if (lane == 0) {            // however the list ended, copies in flight land before the shared memory goes
                 const uint64_t end = global_timer_ns() + 200000000ull;
                 for (int u = max(0, unit - C::kSlots); u < unit; ++u)
                     while (!mbar_try_wait(full(u % C::kSlots), (uint32_t)(u / C::kSlots) & 1) && global_timer_ns() < end) {
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             static_assert(kBatches == 1 || kBatch * kGap % 8 == 0, "swizzle of the batches");
             int unit = 0;
             bool ok = true;
-            while (ok && get()) {
+            while (ok && get_together(6, 128, (warp & 3) == 0)) {
                 if (w.steps == 0) continue;
                 look_up(0);
                 fetch(0, 0);
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
         const int mates = 8 + 4 * t + (warp & 3);                    // barrier of the two warps that share 32 rows
         int used = 0, finished = 0;                                  // uses of sfull, of ofull
         bool ok = true;
-        while (ok && get()) {
+        while (ok && get_together(2 + t, 256, (warp & 7) == 0)) {
         const bool real = row < w.rows;
         const int tok = real ? (w.row0 + row) / p.G : 0;
         const int see = real ? w.first + tok + 1 : 0;                // keys 0 .. see - 1 are seen
