@@ -136,7 +136,7 @@ class Rotary:
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
-                       original: int = 8192, low: float = 1.0, high: float = 4.0) -> Tuple[torch.Tensor, float]:
+                       original: int = 8192, low: float = 1.0, high: Optional[float] = None) -> Tuple[torch.Tensor, float]:
     """(frequencies float64 [rot / 2] on the CPU, amplitude) for `rot` rotated channels: base^(-2i / rot), scaled for
     contexts `factor` times as long as the `original` ones:
       None       as they are;
@@ -145,7 +145,8 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] =
       "bands"    by the turns a pair makes over the original context: below `low` divided by factor, above `high`
                  as they are, in between a blend linear in the turns;
       "yarn"     the same between `low` and `high` turns, but the blend linear in the pair's index, and amplitude
-                 0.1 ln(factor) + 1."""
+                 0.1 ln(factor) + 1.
+    `high` is 4 for "bands" and 32 for "yarn" unless given."""
     if rot < 2 or rot % 2 or base <= 0 or factor < 1 or original < 1:
         raise ValueError("rotary_frequencies: rot even and >= 2, base > 0, factor >= 1, original >= 1")
     i = torch.arange(rot // 2, dtype=torch.float64)
@@ -160,6 +161,8 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] =
         return f / factor, 1.0
     if scaling not in ("bands", "yarn"):
         raise ValueError(f"rotary_frequencies: unknown scaling {scaling!r}")
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
     if not 0 < low < high:
         raise ValueError("rotary_frequencies: 0 < low < high")
     turns = original * f / (2 * math.pi)
