@@ -1,5 +1,5 @@
 """The attention operators where their inputs are unusual: copied cache handles, row tiles without
-keys between others.  (The operators themselves:
+keys between others, queries with a few large channels.  (The operators themselves:
 test_gpu_attn.py, whose helpers are used here.)"""
 import copy
 import pickle
@@ -8,7 +8,9 @@ import numpy as np
 import pytest
 import torch
 
+import attn_ref as ref
 import w4a8_integer_gemm_b200 as q
+from attn_norm import norm_tolerance
 from test_gpu_attn import Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _rng
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +68,45 @@ def test_row_tiles_without_keys(d):
     for _ in range(20):
         assert torch.equal(q.qattn_prompt_attention(qd, kd, vd, cu).view(torch.int16), o.view(torch.int16))
         assert torch.equal(q.qattn_paged_attention(qd, c, *b.dev, max_new=200).view(torch.int16), p.view(torch.int16))
+
+
+def _cached(b, c, s, h, bits):
+    """Keys, values (FP64) of sequence s and KV head h, and which tokens are there."""
+    kc, vc, kp, vp = (t.cpu().numpy() for t in (c.k_codes, c.v_codes, c.k_par, c.v_par))
+    at = [b.place(s, p) for p in range(max(b.kv[s], 0))]
+    there = np.array([p is not None for p in at], dtype=bool)
+    pg, off = (np.array([p[i] if p else 0 for p in at], dtype=int) for i in (0, 1))
+    k, v = (np.where(there[:, None], ref.values64(x[pg, h, off], y[pg, h, off], bits), 0) for x, y in ((kc, kp), (vc, vp)))
+    return k, v, there
+
+
+def _norm_errors(b, c, Q, Hkv, bits, scale, got, **rounded):
+    """The largest error in the norm of a row of `got`, in units of its tolerance."""
+    G, most = Q.shape[1] // Hkv, 0.0
+    for s in range(len(b.new)):
+        t = np.arange(b.cu[s], b.cu[s + 1])
+        for h in range(Hkv if len(t) else 0):
+            k, v, there = _cached(b, c, s, h, bits)
+            seen = there[None] & (np.arange(len(there))[None] <= b.pos[t][:, None])
+            for g in range(G):
+                o, tol = norm_tolerance(Q[t, h * G + g].astype(np.float64), k, v, seen, scale, **rounded)
+                err = np.linalg.norm(got[t, h * G + g].astype(np.float64) - o, axis=-1)
+                most = max(most, float((err / tol).max()))
+    return most
+
+
+@pytest.mark.parametrize("times", [1, 30, 100, 300])
+@pytest.mark.parametrize("new,kv,Hq,d,bits", [([1, 1], [2000, 515], 8, 128, 4), ([1], [3000], 4, 64, 8), ([1], [1200], 32, 128, 8),
+                                              ([2, 5], [900, 400], 6, 64, 4)])
+def test_queries_with_large_channels(new, kv, Hq, d, bits, times):
+    """Few rows, a channel of q as many times the rest as is said and small in the keys: the other channels, which decide
+    the scores, keep their bits."""
+    Hkv = 2
+    b = Batch(new, kv, 16, seed=times)
+    c = _filled_pool(b, Hkv, d, bits, seed=7)
+    Q = _half(_rng(8), b.T, Hq, d)
+    quiet = int(np.abs(_cached(b, c, 0, 0, bits)[0]).mean(0).argmin())
+    Q[..., quiet] = (Q[..., quiet].astype(np.float32) * times).astype(np.float16)
+    o = q.qattn_paged_attention(_dev(Q), c, *b.dev, max_new=max(new))
+    worst = _norm_errors(b, c, Q, Hkv, bits, d ** -0.5, o.cpu().numpy())
+    assert worst < 1, worst

@@ -15,8 +15,12 @@
 //     S^T[token][row]   = codes of K (A, tokens x channels) x q (B), m16n8k32 on
 //                         integers, exact: the codes are 8-bit operands after one
 //                         mask each (none for 8 bits; FP16 operands took four times
-//                         the instructions), and q is two 8-bit digits, 2^-15 of the
-//                         row's largest |q|
+//                         the instructions), and q is three 8-bit digits, whole
+//                         multiples of 2^-21 of the power of two below the row's
+//                         largest |q|: nothing is lost of a channel down to 2^-11 of
+//                         it, and of a smaller one less than FP32 sums lose.  (Two
+//                         digits lose half of a small channel's bits as soon as one
+//                         channel is 100 times the rest.)
 //     O^T[channel][row] = codes of V^T (A, channels x tokens) x p s (B), m16n8k16, FP16
 // Which channel sits at which fragment position does not matter as long as
 // q, and O's write-out, agree; so a lane reads neighbouring bytes of a key or
@@ -60,6 +64,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+// The lowest digit's products sum to less than 2^22 (128 channels of 255 * 128): on top of the bits of 1.5 * 2^23 they
+// are an FP32 number's last bits, and their conversion is a subtraction.
+constexpr int kLowBase = 0x4B400000;
 constexpr int kSwitch = 2;              // granules that a run counts for its beginning and end
 constexpr int kLeast = 4;               // granules of a warp's share, at least (a partial result costs about as much)
 
@@ -265,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
         const int t_seq = __ldg(a.cu + b);
         const int tok0 = 16 * g0, tok1 = min(16 * g1, len);
 
-        // ---- q: two 8-bit digits per channel, sums, limits of the lane's columns ----
-        uint32_t qf[NT][2][D / 32][2];                   // [.][high, low digit][MMA step][fragment register]
+        // ---- q: three 8-bit digits per channel, sums, limits of the lane's columns ----
+        uint32_t qf[NT][3][D / 32][2];                   // [.][digit, highest first][MMA step][fragment register]
         float sq[NT][2], qs[NT][2];                      // sum of q, value of a unit of its digits; log2 units
         float m[NT][2], l[NT][2], W[NT][2];
         float k = 0.0f;                                  // power of two on the value scales; 0: none seen yet
@@ -308,30 +315,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float inv = top > 0.0f ? 16256.0f / top : 0.0f;
+            // 2^e <= top (an FP16 number, normal in FP32; a row of zeros: as the smallest): in units of 2^(e - 21)
+            const int e = max((int)(__float_as_uint(top) >> 23), 127 - 24) - 127;
+            const float inv = __uint_as_float((uint32_t)(127 + 21 - e) << 23);
             int s = 0;                                   // of the digits: q's rounding then meets s c + m, not s c alone
 #pragma unroll
             for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t hi = 0, lo = 0;
+                    uint32_t dig[3] = {0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int v = __float2int_rn(__half2float(x[j][h][i]) * inv);    // -16256 .. 16256
+                        const int v = __float2int_rn(__half2float(x[j][h][i]) * inv);    // below 2^22 in size
+                        const int v1 = (v + 128) >> 8, v2 = (v1 + 128) >> 8;             // v = 256 v1 + (-128 .. 127), and so on
                         s += v;
-                        const int d = (v + 64) >> 7;                                     // v = 128 d + (-64 .. 63)
-                        hi |= (uint32_t)(d & 0xFF) << (8 * i);
-                        lo |= (uint32_t)((v - 128 * d) & 0xFF) << (8 * i);
+                        dig[0] |= (uint32_t)(v2 & 0xFF) << (8 * i);
+                        dig[1] |= (uint32_t)(v1 & 0xFF) << (8 * i);
+                        dig[2] |= (uint32_t)(v & 0xFF) << (8 * i);
                     }
-                    qf[t][0][j][h] = hi;
-                    qf[t][1][j][h] = lo;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) qf[t][k][j][h] = dig[k];
                 }
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int col = 8 * t + 2 * c + u;
-                qs[t][u] = __shfl_sync(0xffffffffu, top, (2 * c + u) * 4) * (p.scale_log2 / 16256.0f);
+                qs[t][u] = __uint_as_float((uint32_t)(127 - 21 + __shfl_sync(0xffffffffu, e, (2 * c + u) * 4)) << 23) * p.scale_log2;
                 sq[t][u] = (float)__shfl_sync(0xffffffffu, s, (2 * c + u) * 4) * qs[t][u];
                 const bool real = col < rows;            // others' results go nowhere
                 see[t][u] = real ? first + (run.row0 + col) / p.G + 1 : 1 << 30;
@@ -410,14 +420,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 vp[i][0] = x.z;
                 vp[i][1] = x.w;
             }
-            // q . codes, exact in 32-bit integers
-            int acc[C::kGr][NT][2][4];
+            // q . codes: each digit's products exact in 32-bit integers, and joined in FP32
+            float dot[C::kGr][NT][4];
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i) {
+                int acc[NT][3][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) acc[i][t][r / 4][r % 4] = 0;
+                    for (int r = 0; r < 12; ++r) acc[t][r / 4][r % 4] = r < 8 ? 0 : kLowBase;
                 uint32_t kw[2][C::kKW];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -441,10 +452,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        mma16832(acc[i][t][0], f, qf[t][0][j][0], qf[t][0][j][1]);
-                        mma16832(acc[i][t][1], f, qf[t][1][j][0], qf[t][1][j][1]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) mma16832(acc[t][k], f, qf[t][k][j][0], qf[t][k][j][1]);
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        dot[i][t][r] = fmaf((float)(acc[t][0][r] * 256 + acc[t][1][r]), 256.0f,
+                                            __int_as_float(acc[t][2][r]) - __int_as_float(kLowBase));
             }
             // Tokens that no row sees may hold anything: their parameters become zeros, so that nothing below is NaN.
             const bool edge = tok + C::kGroup > see_min || gone[0] || gone[C::kGr - 1];
@@ -476,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        sc[i][t][r] = fmaf((float)(acc[i][t][0][r] * 128 + acc[i][t][1][r]), ks[r >> 1] * qs[t][r & 1],
-                                           fmaf(km[r >> 1], sq[t][r & 1], base[t][r & 1]));
+                        sc[i][t][r] = fmaf(dot[i][t][r], ks[r >> 1] * qs[t][r & 1], fmaf(km[r >> 1], sq[t][r & 1], base[t][r & 1]));
             }
             if (edge) {
 #pragma unroll
