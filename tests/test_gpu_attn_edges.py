@@ -1,5 +1,6 @@
 """The attention operators where their inputs are unusual: copied cache handles, row tiles without
-keys between others, queries with a few large channels.  (The operators themselves:
+keys between others, queries with a few large channels,
+mass in the tail of the weights.  (The operators themselves:
 test_gpu_attn.py, whose helpers are used here.)"""
 import copy
 import pickle
@@ -11,7 +12,7 @@ import torch
 import attn_ref as ref
 import w4a8_integer_gemm_b200 as q
 from attn_norm import norm_tolerance
-from test_gpu_attn import Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _rng
+from test_gpu_attn import Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _poisoned_pool, _rng
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,56 @@ def test_queries_with_large_channels(new, kv, Hq, d, bits, times):
     o = q.qattn_paged_attention(_dev(Q), c, *b.dev, max_new=max(new))
     worst = _norm_errors(b, c, Q, Hkv, bits, d ** -0.5, o.cpu().numpy())
     assert worst < 1, worst
+
+
+def _tail_case(n, d, first):
+    """Keys and values [n, d]: one token (the first, or one in the middle) that outweighs each other by 2^27 to 2^31 for a
+    query of ones, with values of zero; the others have no scores and large values, the same in every channel, so
+    that a 4- or 8-bit row holds them exactly."""
+    k, v = np.zeros((n, d), np.float16), np.zeros((n, d), np.float16)
+    v[:] = (40000 + 64 * (np.arange(n) % 300))[:, None].astype(np.float16)
+    at = 0 if first else n // 2
+    k[at] = np.float16(29 * np.log(2) / d ** 0.5)
+    v[at] = 0
+    return k, v
+
+
+def _check_tail(q_rows, k, v, pos, got, scale):
+    """Within attn_ref's bound and what rounding the weights costs below FP16's normal numbers: half a step, 2^-25, of
+    a weight of one, 2^-8 of the largest: 2^-33 of it each, times the values."""
+    k, v = k.astype(np.float64), v.astype(np.float64)
+    for i, p in enumerate(pos):
+        seen = (np.arange(len(k)) <= p)[None]
+        o, tol = ref.attend(q_rows[i:i + 1].astype(np.float64), k, v, seen, scale)
+        largest = 1.0                                         # the weights' sum is the largest one's within 2^-10
+        err = np.abs(got[i].astype(np.float64) - o[0])
+        assert np.all(err <= tol[0] + 2.0 ** -33 * largest * (np.abs(v) * seen[0][:, None]).sum(0)), (i, float(err.max()))
+        assert o.min() > 0.05                                 # (the tail is what the output consists of)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_mass_in_the_tail_of_a_prompt(d, first):
+    n, scale = 4000, d ** -0.5
+    k, v = _tail_case(n, d, first)
+    X = np.zeros((n, 3, d), np.float16)
+    X[:, 0] = (0.95 + 0.1 * _rng(1).random(n))[:, None]
+    X[:, 1], X[:, 2] = k, v
+    o = q.qattn_prompt_attention(*_dev(X).split([1, 1, 1], 1), _dev(np.array([0, n], np.int32))).cpu().numpy()
+    at = np.array([2900, 3071, 3500, 3999])
+    _check_tail(X[at, 0], k, v, at, o[at, 0], scale)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("d,bits", [(64, 4), (128, 4), (128, 8)])
+def test_mass_in_the_tail_of_a_cache(d, bits, first):
+    n, new, scale = 9000, 64, d ** -0.5
+    k, v = _tail_case(n, d, first)
+    b = Batch([n], [n], 64, seed=2)
+    c = _poisoned_pool(b, 1, d, bits)
+    q.qattn_cache_append(_dev(k[:, None]), _dev(v[:, None]), c, *b.dev)
+    Q = np.repeat((0.95 + 0.1 * _rng(2).random(new))[:, None, None], d, 2).astype(np.float16)
+    cu = _dev(np.array([0, new], np.int32))
+    o = q.qattn_paged_attention(_dev(Q), c, b.dev[0], cu, b.dev[2]).cpu().numpy()
+    at = np.array([0, 31, 63])
+    _check_tail(Q[at, 0], k, v, n - new + at, o[at, 0], scale)

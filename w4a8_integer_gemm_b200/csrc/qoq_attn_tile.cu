@@ -184,6 +184,11 @@ __device__ __forceinline__ void ex2_pair(float &x, float &y)
 // A cache's loaders need that pipe themselves: 236 us with none, 241 with two.)
 constexpr int kPoly = 3;
 
+// How far below the true maximum the one in use is set, in log2 units: weights count in P down to 2^-25 of one, so down to
+// 2^-33 of the largest (a context of 2^17 tokens can hold 2^-16 of its mass below that; at 2^-25, 2^-8), and with full
+// FP16 precision down to 2^-22.  64 weights of the largest's size sum to 2^14 then, a quarter of what they may.
+constexpr float kBelow = 8.0f;
+
 // byte offset of 16-byte vector `vec` of row `row` in a [rows][64 channels] block, 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int row, int vec)
 {
@@ -762,9 +767,9 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     if (c >= left) x[c] = 0xFF800000u;
             };
             // P = 2^(s - m), FP16, with the maximum in use, 16 columns at a time, the next 16 on their way from tensor
-            // memory.  The maximum may lag far behind: as long as a thread's weights sum to at most 2^14 they fit FP16,
-            // and no maximum has to be taken.  Otherwise, and for the first keys that a row sees, the two warps of the
-            // rows take it, rescale what they have and weigh the tile again.
+            // memory.  The maximum may lag behind: as long as a thread's weights sum to what FP16 holds, each of them
+            // fits, and no maximum has to be taken.  Otherwise, and for the first keys that a row sees, the two warps of
+            // the rows take it (less kBelow), rescale what they have and weigh the tile again.
             uint32_t pk[kCols / 2];
             for (int round = 0;; ++round) {
                 if (round > 0 || i > 0) {                            // (an item's first keys have no maximum to use)
@@ -800,7 +805,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     unpair(add2(sum2[0], sum2[1]), s0, s1);
                     s0 += s1;
                     // (also: everyone has read S before anyone writes P over it)
-                    const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 16384.0f || high > 14.0f || (m == -INFINITY && lim > 0)));
+                    const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 65504.0f || high > 15.0f || (m == -INFINITY && lim > 0)));
                     if (!again) {
                         l += s0;
                         break;
@@ -817,7 +822,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                 }
                 s_row[t][h][r] = top * sl;
                 named_barrier(mates, 64);
-                const float m1 = fmaxf(m, fmaxf(s_row[t][0][r], s_row[t][1][r]));
+                const float m1 = fmaxf(m, fmaxf(s_row[t][0][r], s_row[t][1][r]) - kBelow);
                 const float keep = m == -INFINITY ? 0.0f : ex2(m - m1);
                 m = m1;
                 l *= keep;
