@@ -1,6 +1,7 @@
 """The attention operators where their inputs are unusual: copied cache handles, row tiles without
 keys between others, queries with a few large channels,
-mass in the tail of the weights.  (The operators themselves:
+mass in the tail of the weights; and whether every token
+of a long context counts, once.  (The operators themselves:
 test_gpu_attn.py, whose helpers are used here.)"""
 import copy
 import pickle
@@ -12,7 +13,7 @@ import torch
 import attn_ref as ref
 import w4a8_integer_gemm_b200 as q
 from attn_norm import norm_tolerance
-from test_gpu_attn import Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _poisoned_pool, _rng
+from test_gpu_attn import DEV, Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _poisoned_pool, _rng
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,66 @@ def test_mass_in_the_tail_of_a_cache(d, bits, first):
     o = q.qattn_paged_attention(_dev(Q), c, b.dev[0], cu, b.dev[2]).cpu().numpy()
     at = np.array([0, 31, 63])
     _check_tail(Q[at, 0], k, v, n - new + at, o[at, 0], scale)
+
+
+# ------------------------------------------------------ every token counted ----
+def _marked_cache(b, Hkv, d, bits):
+    """A cache whose values mark their 16-token granule: granule n of a sequence has ones in channel 5 n mod d."""
+    c = _poisoned_pool(b, Hkv, d, bits)
+    V = np.zeros((sum(b.kv), 1, d), np.float16)
+    at = 0
+    for n in b.kv:
+        V[at + np.arange(n), 0, 5 * (np.arange(n) // 16) % d] = 1
+        at += n
+    r = _rng(1)
+    K = _half(r, sum(b.kv), 1, d)
+    cu = _dev(np.concatenate([[0], np.cumsum(b.kv)]).astype(np.int32))
+    K, V = (_dev(np.repeat(x, Hkv, 1)) for x in (K, V))
+    q.qattn_cache_append(K, V, c, b.dev[0], cu, b.dev[2])
+    return c
+
+
+@pytest.mark.parametrize("G,new,kv,d,bits", [
+    (4, [1], [20000], 128, 4), (4, [1], [7777], 128, 8), (1, [1, 1, 1], [131, 20011, 4999], 64, 4), (16, [1, 1], [30000, 16], 128, 4),
+    (32, [1], [9001], 64, 8), (8, [1] * 40, [300 + 211 * i for i in range(40)], 128, 4), (4, [3, 8], [5000, 7000], 64, 4),
+    (8, [64], [20000], 128, 4), (4, [300, 70], [7777, 15001], 64, 8), (1, [513, 1, 40], [6000, 9000, 3000], 128, 8), (64, [1], [12000], 128, 4)])
+def test_every_token_counts_once(G, new, kv, d, bits):
+    """Queries of zeros weigh all tokens alike, so a channel of the output is the share of its granules' tokens: a granule
+    that is left out or counted twice at a cut moves it by 6% or more here, a single token by 2^-8 or more."""
+    Hkv = 2
+    b = Batch(new, kv, 16, seed=G)
+    c = _marked_cache(b, Hkv, d, bits)
+    Q = torch.zeros(b.T, G * Hkv, d, dtype=torch.float16, device=DEV)
+    for hint in (max(new), None, 1):
+        o = q.qattn_paged_attention(Q, c, *b.dev, max_new=hint).cpu().numpy().astype(np.float64)
+        for t in range(b.T):
+            n = b.pos[t] + 1
+            count = np.bincount(5 * (np.arange(n) // 16) % d, minlength=d)
+            one = _one(bits)                                  # what the cache makes of a one among zeros
+            want = one * count / n
+            # weights of 1 and codes are exact operands; the cached one in FP16 (tiles) and the output are rounded.  FP32:
+            # centred, every token adds half a one to every channel, and its half comes off again; up to 2^7 additions
+            # in a share round by 2^-25 of what they have got to
+            tol = (2 * ref.HALF_STEP + 2.0 ** -20) * want + 2.0 ** -18 * one / 2 + 2.0 ** -25
+            assert np.all(np.abs(o[t] - want[None]) <= tol[None]), (hint, t, float((np.abs(o[t] - want) / tol).max()))
+
+
+def _one(bits):
+    code, s, m = ref.quantise(np.array([0.0, 1.0], np.float16), bits)
+    return float(code[1]) * float(s) + float(m)
+
+
+@pytest.mark.parametrize("new,kv,page,Hkv,Hq,d,bits,absent", [
+    ([1, 1], [20000, 7777], 128, 2, 14, 128, 4, [(0, 7)]), ([1, 1], [9000, 300], 32, 1, 32, 64, 8, []),
+    ([3, 5], [15000, 2000], 64, 2, 8, 128, 8, []), ([70, 1], [20000, 4000], 64, 1, 8, 128, 4, []),
+    ([40, 64], [9000, 1200], 16, 1, 7, 64, 8, [(0, 3)]), ([130, 3], [6000, 800], 32, 2, 4, 128, 8, [])])
+def test_errors_in_the_norm(new, kv, page, Hkv, Hq, d, bits, absent):
+    """Long contexts, where a token lost at a cut is beyond the bound (test_attn_norm.py)."""
+    b = Batch(new, kv, page, seed=d, absent=absent)
+    c = _filled_pool(b, Hkv, d, bits, seed=bits)
+    Q = _half(_rng(11), b.T, Hq, d)
+    for hint in (max(new), 1):
+        o = q.qattn_paged_attention(_dev(Q), c, *b.dev, max_new=hint)
+        tiles = hint > 1 and max(new) * Hq // Hkv > 32        # (tiles round the cached keys and values to FP16)
+        worst = _norm_errors(b, c, Q, Hkv, bits, d ** -0.5, o.cpu().numpy(), keys=tiles, values=tiles)
+        assert worst < 1, (hint, worst)
