@@ -27,8 +27,12 @@
  *     Hkv, Hq / Hkv <= 64, Hq <= 1024.
  *   - 16-byte aligned pointers (index arrays: 4-byte). T <= 2^21 rows,
  *     B <= 65536, pages >= 1, table_pages * page_size <= 2^24.
- *   - Inputs are finite. Tokens that a row does not see (later tokens of its
- *     own prompt apart) do not reach it, whatever they hold.
+ *   - Infinities and NaN in the rows are not hidden: a cached row with one
+ *     stands for d NaN, and a row of q with one, or one that sees a key with
+ *     a NaN or a value with either, gives outputs that are not finite (of a
+ *     prompt's values: in their channel).
+ *     Tokens that a row does not see (later new tokens of its own sequence
+ *     apart) do not reach it, whatever they hold.
  *   - T, B == 0 are valid empty problems: QOQ_OK, nothing launched.
  *   - Index arrays are read on the device and checked there: an index that
  *     points outside its array skips the access, as said below.

@@ -1,7 +1,7 @@
 """The attention operators where their inputs are unusual: copied cache handles, row tiles without
 keys between others, queries with a few large channels,
 mass in the tail of the weights; and whether every token
-of a long context counts, once.  (The operators themselves:
+of a long context counts, once; NaN and infinities.  (The operators themselves:
 test_gpu_attn.py, whose helpers are used here.)"""
 import copy
 import pickle
@@ -13,7 +13,7 @@ import torch
 import attn_ref as ref
 import w4a8_integer_gemm_b200 as q
 from attn_norm import norm_tolerance
-from test_gpu_attn import DEV, Batch, _check_paged, _check_prompt, _dev, _filled_pool, _half, _poisoned_pool, _rng
+from test_gpu_attn import DEV, Batch, _check_paged, _check_prompt, _dev, _filled_pool, _freq, _half, _poisoned_pool, _rng
 
 pytestmark = pytest.mark.gpu
 
@@ -228,3 +228,121 @@ def test_errors_in_the_norm(new, kv, page, Hkv, Hq, d, bits, absent):
         tiles = hint > 1 and max(new) * Hq // Hkv > 32        # (tiles round the cached keys and values to FP16)
         worst = _norm_errors(b, c, Q, Hkv, bits, d ** -0.5, o.cpu().numpy(), keys=tiles, values=tiles)
         assert worst < 1, (hint, worst)
+
+
+# ------------------------------------------------------------ not finite ----
+BAD = {"nan": float("nan"), "inf": float("inf"), "-inf": float("-inf")}
+
+
+@pytest.mark.parametrize("what", list(BAD))
+@pytest.mark.parametrize("d,bits,rot", [(64, 4, 0), (128, 4, 128), (128, 8, 32), (64, 8, 64)])
+def test_append_keeps_what_is_not_finite(d, bits, rot, what):
+    """Every value of a cached row with a NaN or an infinity reads back as one; the other rows are as without it."""
+    Hkv, n = 3, 70
+    b = Batch([n], [n + 5], 16, seed=d)
+    x = _half(_rng(d + bits), n, 2 * Hkv, d)
+    y = x.copy()
+    bad = np.zeros((n, 2 * Hkv), dtype=bool)
+    for t, h, ch in ((0, 0, [0]), (3, 4, [d - 1]), (n - 1, 5, [d // 2]), (17, 2, range(0, d, 5)), (30, 1, range(d)), (31, 3, range(d))):
+        y[t, h, list(ch)] = BAD[what]
+        bad[t, h] = True
+    y[40, 1, :2], bad[40, 1] = [float("inf"), float("-inf")], True
+    got = []
+    for rows in (x, y):
+        c = _poisoned_pool(b, Hkv, d, bits)
+        rotary = q.Rotary(_dev(_freq(rot))) if rot else None
+        xd = _dev(rows)
+        q.qattn_cache_append(xd[:, :Hkv], xd[:, Hkv:], c, *b.dev, rotary=rotary)
+        got.append(np.concatenate([t.cpu().numpy() for t in q.qattn_cache_read(c, *b.dev, n)], 1))
+    assert np.array_equal(got[0][~bad], got[1][~bad]) and np.isfinite(got[0]).all()
+    assert np.isnan(got[1][bad]).all()
+
+
+PLACES = [  # new, kv, Hq, Hkv, d, bits, hint: a run in one warp, runs over warps and CTAs, 16 rows, tiles of one CTA and of several
+    ([1], [40], 4, 1, 64, 4, 1), ([1, 1], [9000, 40], 8, 2, 128, 4, 1), ([1] * 30, [2000] * 30, 8, 2, 128, 8, 1), ([2, 1], [3000, 90], 32, 2, 64, 8, 2),
+    ([60, 1], [9000, 300], 8, 2, 128, 4, None), ([300, 40], [500, 40], 4, 2, 64, 8, 300), ([50], [70], 2, 1, 128, 8, 50)]
+
+
+@pytest.mark.parametrize("new,kv,Hq,Hkv,d,bits,hint", PLACES)
+def test_paged_attention_keeps_what_is_not_finite(new, kv, Hq, Hkv, d, bits, hint):
+    """A row of q with a NaN or an infinity, and the rows that see a cached key or value row with one, come out as NaN or
+    infinities throughout.  Other sequences and KV heads have the bits that they have without it.  Rows of the same work
+    item may have their maximum taken at other times, so that the weights' and the output's roundings differ: by 2^-11 of
+    the largest value each, in either call."""
+    b = Batch(new, kv, 16, seed=d)
+    c = _filled_pool(b, Hkv, d, bits, seed=3)
+    Q = _half(_rng(4), b.T, Hq, d)
+    G = Hq // Hkv
+
+    def run(Q):
+        return q.qattn_paged_attention(_dev(Q), c, *b.dev, max_new=hint).cpu().numpy()
+
+    clean = run(Q)
+    assert np.isfinite(clean).all()
+    near = 2.0 ** -8 * max(float(np.abs(_cached(b, c, s, h, bits)[1]).max()) for s in range(len(new)) for h in range(Hkv))
+    for value in BAD.values():
+        for row, head, ch in ((0, 0, 0), (b.T - 1, Hq - 1, d - 1), (b.T // 2, Hq // 2, d // 2)):
+            Z = Q.copy()
+            Z[row, head, ch] = value
+            o = run(Z)
+            hit = np.zeros((b.T, Hq), dtype=bool)
+            hit[row, head] = True
+            assert not np.isfinite(o[hit]).any()
+            assert np.abs(o[~hit].astype(np.float64) - clean[~hit].astype(np.float64)).max() <= near
+            hit[b.seq == b.seq[row], head // G * G:head // G * G + G] = True     # what shares work items with it
+            assert np.array_equal(o[~hit], clean[~hit])
+    old = min(b.kv[0] - b.new[0], 37)                         # a token that every row of the sequence sees
+    for token in sorted({0, old, max(0, b.kv[0] - b.new[0] - 1)}):
+        page, off = b.place(0, token)
+        for par in (c.k_par, c.v_par):
+            kept = par[page, Hkv - 1, off].clone()
+            par[page, Hkv - 1, off] = float("nan")
+            o = run(Q)
+            hit = np.zeros((b.T, Hq), dtype=bool)
+            hit[:b.new[0], (Hkv - 1) * G:] = True
+            assert np.array_equal(o[~hit], clean[~hit])
+            assert not np.isfinite(o[hit]).any(), token
+            par[page, Hkv - 1, off] = kept
+    assert np.array_equal(run(Q), clean)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 1), (128, 3, 3)])
+def test_prompt_attention_keeps_nan(d, Hq, Hkv):
+    """A NaN key (each column of a key tile in turn) makes the rows that see it NaN, a NaN or infinite value its channel, a
+    row of q with one itself; other prompts and KV heads keep their bits, other rows their values up to the roundings of
+    weights and outputs (2^-11 of the largest value each, in either call)."""
+    lens = [300, 270]
+    T, G = sum(lens), Hq // Hkv
+    X = _half(_rng(d), T, Hq + 2 * Hkv, d)
+    cu = _dev(np.array([0, 300, T], np.int32))
+
+    def run(X):
+        return q.qattn_prompt_attention(*_dev(X).split([Hq, Hkv, Hkv], 1), cu).cpu().numpy()
+
+    clean = run(X)
+    near = 2.0 ** -8 * float(np.abs(X[:, Hq + Hkv:]).max())
+    first = np.arange(T) < 300
+    for j in list(range(0, 16)) + [63, 64, 127, 128, 140, 299]:
+        Z = X.copy()
+        Z[j, Hq + Hkv - 1, j % d] = np.nan
+        o = run(Z)
+        sees = first & (np.arange(T) >= j)
+        assert not np.isfinite(o[sees, (Hkv - 1) * G:]).any(), j
+        assert np.array_equal(o[~first], clean[~first]) and np.array_equal(o[:, :(Hkv - 1) * G], clean[:, :(Hkv - 1) * G])
+        # (a masked key only makes masked scores)
+        assert not j or np.abs(o[:j].astype(np.float64) - clean[:j].astype(np.float64)).max() <= near
+    for value in (np.nan, np.inf):
+        Z = X.copy()
+        Z[20, Hq + 2 * Hkv - 1, 5] = value
+        o = run(Z)
+        assert not np.isfinite(o[20:300, (Hkv - 1) * G:, 5]).any() and np.array_equal(o[300:], clean[300:])
+        other = np.arange(d) != 5
+        assert np.array_equal(o[..., other], clean[..., other])
+        Z = X.copy()
+        Z[33, 0, 7] = value
+        o = run(Z)
+        hit = np.zeros((T, Hq), dtype=bool)
+        hit[33, 0] = True
+        assert not np.isfinite(o[hit]).any()
+        assert np.abs(o[~hit].astype(np.float64) - clean[~hit].astype(np.float64)).max() <= near
+        assert np.array_equal(o[300:], clean[300:]) and np.array_equal(o[:, G:], clean[:, G:])

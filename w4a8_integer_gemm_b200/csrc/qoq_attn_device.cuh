@@ -54,6 +54,21 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, volati
     return true;
 }
 
+// Minimum and maximum that are NaN where an operand is.
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b)
 {
     uint32_t r;

@@ -311,13 +311,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    top = fmaxf(top, fabsf(__half2float(x[j][e / 4][e & 3])));
+                    top = max_nan(top, fabsf(__half2float(x[j][e / 4][e & 3])));
                 }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e <= top (an FP16 number, normal in FP32; a row of zeros: as the smallest): in units of 2^(e - 21)
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^e <= top (an FP16 number, normal in FP32; a row of zeros: as the smallest): in units of 2^(e - 21), or of
+            // NaN where the row is not finite
+            const bool finite = top <= 65504.0f;
             const int e = max((int)(__float_as_uint(top) >> 23), 127 - 24) - 127;
-            const float inv = __uint_as_float((uint32_t)(127 + 21 - e) << 23);
+            const float inv = finite ? __uint_as_float((uint32_t)(127 + 21 - e) << 23) : 0.0f;
+            const float unit = finite ? __uint_as_float((uint32_t)(127 - 21 + e) << 23) : __uint_as_float(0x7FC00000u);
             int s = 0;                                   // of the digits: q's rounding then meets s c + m, not s c alone
 #pragma unroll
             for (int j = 0; j < D / 32; ++j)
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int col = 8 * t + 2 * c + u;
-                qs[t][u] = __uint_as_float((uint32_t)(127 - 21 + __shfl_sync(0xffffffffu, e, (2 * c + u) * 4)) << 23) * p.scale_log2;
+                qs[t][u] = __shfl_sync(0xffffffffu, unit, (2 * c + u) * 4) * p.scale_log2;
                 sq[t][u] = (float)__shfl_sync(0xffffffffu, s, (2 * c + u) * 4) * qs[t][u];
                 const bool real = col < rows;            // others' results go nowhere
                 see[t][u] = real ? first + (run.row0 + col) / p.G + 1 : 1 << 30;
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     v[2 * mt + 1] = fmaf(o[t][mt][2 + u], inv_k, y);
                 }
                 if (begins && ends) {
-                    const float inv = x > 0.0f ? 1.0f / x : 0.0f;
+                    const float inv = x == 0.0f ? 0.0f : 1.0f / x;      // (not for a sum that is NaN)
                     const int r = run.row0 + col;
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(t_seq + r / p.G) * p.ldo +
                                                            (size_t)(hk * p.G + r % p.G) * D + (D / 8) * g);
@@ -671,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
                     for (int i = 0; i < C::kMt / 2; ++i)
                         reinterpret_cast<float4 *>(dst + (D / 8) * g)[i] =
                             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    if (g == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(m[t][u], x);
+                    // (a sum that is NaN counts whatever its maximum: the joins skip parts that saw nothing by theirs)
+                    if (g == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(x == x ? m[t][u] : 0.0f, x);
                 }
             }
         // the warp whose share holds the run's first granule
@@ -796,7 +800,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const RowsArgs
                                     fmaf(y[u].w, g[u], v.w));
             }
         }
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         const int r = j.y + row;
         const __half2 h0 = __floats2half2_rn(v.x * inv, v.y * inv), h1 = __floats2half2_rn(v.z * inv, v.w * inv);
         if (lane < D / 4)

@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                             float e0, e1;
                             unpair(fma2(pair(__uint_as_float(y[2 * u]), __uint_as_float(y[2 * u + 1])), sl2, sub2), e0, e1);
                             if (BITS == 0 && u < kPoly) {
-                                high = fmaxf(fmaxf(high, e0), e1);       // (a sum would not show what is out of its range)
+                                high = max_nan(max_nan(high, e0), e1);   // (a sum would not show what is out of its range, or NaN)
                                 ex2_pair(e0, e1);
                             } else {
                                 e0 = ex2(e0);
@@ -803,9 +803,9 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                     float s0, s1;
                     unpair(add2(sum2[0], sum2[1]), s0, s1);
-                    s0 += s1;
+                    s0 = BITS || high == high ? s0 + s1 : high;
                     // (also: everyone has read S before anyone writes P over it)
-                    const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 65504.0f || high > 15.0f || (m == -INFINITY && lim > 0)));
+                    const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 65504.0f || high > 15.0f || (m == -INFINITY && lim > 0 && s0 == s0)));
                     if (!again) {
                         l += s0;
                         break;
@@ -857,7 +857,8 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
             named_barrier(mates, 64);       // s_row has been read: the next item, without keys for this row tile, writes it at once
             const int g = real ? (w.row0 + row) % p.G : 0;
             if (BITS == 0 || w.slot < 0) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const bool none = BITS && l == 0.0f;                 // the row saw nothing (a sum that is NaN is not hidden)
+                const float inv = none ? 0.0f : 1.0f / l;
                 uint16_t *dst = p.out + (int64_t)(w.t_seq + tok) * p.ldo + (size_t)(w.hk * p.G + g) * D + kOut * h;
 #pragma unroll
                 for (int c = 0; c < kOut; c += 16) {
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
-                        y[u] = l > 0.0f ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                        y[u] = none ? 0u : *reinterpret_cast<const uint32_t *>(&x);
                     }
                     const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
                     if (real) {
@@ -945,7 +946,7 @@ __global__ void __launch_bounds__(kJoinRows *D / 4) attn_tile_join_kernel(const 
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (ml[u].y <= 0.0f) continue;           // saw nothing, and wrote no sums
+            if (ml[u].y == 0.0f) continue;           // saw nothing, and wrote no sums
             const float m1 = fmaxf(M, ml[u].x), f0 = M == -INFINITY ? 0.0f : ex2(M - m1), f1 = ex2(ml[u].x - m1);
             M = m1;
             L = fmaf(L, f0, ml[u].y * f1);
@@ -953,7 +954,7 @@ __global__ void __launch_bounds__(kJoinRows *D / 4) attn_tile_join_kernel(const 
                             fmaf(v.w, f0, x[u].w * f1));
         }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int r = j.y + row;
     uint16_t *dst = out + (int64_t)(t0 + r / G) * ldo + (size_t)(j.z * G + r % G) * D + 4 * at;
     const __half2 y0 = __floats2half2_rn(v.x * inv, v.y * inv), y1 = __floats2half2_rn(v.z * inv, v.w * inv);

@@ -271,16 +271,19 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(
         __half2 lo2 = *reinterpret_cast<const __half2 *>(&w[0]), hi2 = lo2;
 #pragma unroll
         for (int u = 1; u < 8; ++u) {
-            lo2 = __hmin2(lo2, *reinterpret_cast<const __half2 *>(&w[u]));
-            hi2 = __hmax2(hi2, *reinterpret_cast<const __half2 *>(&w[u]));
+            lo2 = __hmin2_nan(lo2, *reinterpret_cast<const __half2 *>(&w[u]));
+            hi2 = __hmax2_nan(hi2, *reinterpret_cast<const __half2 *>(&w[u]));
         }
-        float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
+        float lo = min_nan(__low2float(lo2), __high2float(lo2)), hi = max_nan(__low2float(hi2), __high2float(hi2));
 #pragma unroll
         for (int o = 1; o < kSlots; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
         if (work && !is_q) {
+            // A row that is not finite gets a scale and a minimum of NaN: all its values read back as that, and whoever
+            // sees them knows.
+            if (!(hi - lo <= 2 * 65504.0f)) lo = hi = __uint_as_float(0x7FC00000u);
             const __half sh = __float2half_rz(__fdiv_rn(hi - lo, (float)((1 << BITS) - 1)));
             const float s = __half2float(sh), inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
             const int hk = is_k ? h - Hq : h - Hq - Hkv;
