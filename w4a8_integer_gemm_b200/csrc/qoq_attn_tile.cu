@@ -803,11 +803,11 @@ __global__ void __launch_bounds__(tile_threads(BITS), 1) attn_tile_kernel(const 
                     }
                     float s0, s1;
                     unpair(add2(sum2[0], sum2[1]), s0, s1);
-                    s0 = BITS || high == high ? s0 + s1 : high;
+                    s0 += s1;
                     // (also: everyone has read S before anyone writes P over it)
                     const bool again = named_barrier_any(mates, 64, round == 0 && (s0 > 65504.0f || high > 15.0f || (m == -INFINITY && lim > 0 && s0 == s0)));
                     if (!again) {
-                        l += s0;
+                        l += BITS || high == high ? s0 : high;
                         break;
                     }
                 }
