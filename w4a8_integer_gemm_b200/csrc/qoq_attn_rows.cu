@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_rows_kernel(co
             // Value scales; k brings the largest seen into [2^5, 2^6), so that with p <= 2^8 the products p s k fit FP16.
             // In units of the largest scale, p s has FP16's full precision from 2^-19 on and vanishes below 2^-30: of a
             // token's values only what sets them apart from its m', whose sum is FP32 (2^17 such tokens together move
-            // the output by less than 2^-9 of the largest token's range).
+            // the output by less than 2^-13 of the largest token's range).
             float vs[C::kGr][2], vm[C::kGr][2], vmax = 0.0f;
 #pragma unroll
             for (int i = 0; i < C::kGr; ++i)
