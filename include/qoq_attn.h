@@ -121,10 +121,16 @@ QOQ_API size_t qattn_paged_attention_workspace_bytes(int T, int B, int Hq, int H
  * row i of sequence b sees positions j <= kv_len[b] - n_b + i, and
  *     out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j)
  * with k, v the values the cache stands for. A row that sees nothing gets
- * zeros.
+ * zeros. Sums and the softmax's statistics are FP32, weights are rounded to
+ * FP16, and so is the output. Scores are products of q with the cached codes,
+ * without a rounding in between, for up to 32 rows per sequence and KV head
+ * (n_b * Hq / Hkv); with more, keys and values may be rounded to FP16 first,
+ * to what qattn_cache_read gives: half a step, as of any FP16 key. Weights
+ * below 2^-30 of a row's largest may count as nothing.
  *   max_new    an upper bound of every n_b that the caller knows (T when it
  *              knows none). It only chooses kernels: rows beyond it are
- *              computed all the same.
+ *              computed all the same. A decode step without it takes kernels
+ *              for 16 rows instead of 8, and launches those for chunks.
  *   out        [T][Hq][d] FP16, row stride ldo.
  * The call's rows times its longest context are limited: (T * Hq / 256 +
  * min(T, B) * Hkv) * (table_pages * page_size / 128 + 2) < 2^31 (a table

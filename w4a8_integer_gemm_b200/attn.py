@@ -9,7 +9,7 @@ the name of the C entry point it calls and only marshals arguments.
     cache = paged_kv_cache(pages, Hkv, d, bits=4)
     rot = Rotary(rotary_frequencies(d, base=5e5)[0].cuda())
     q = qattn_cache_append(k, v, cache, table, cu, kv_len, rotary=rot, q=q)
-    o = qattn_paged_attention(q, cache, table, cu, kv_len)  # fp16 [T, Hq, d]
+    o = qattn_paged_attention(q, cache, table, cu, kv_len, max_new=1)  # fp16 [T, Hq, d]; 1: a decode step
 
 The batch: `cu` int32 [B + 1] (row offsets of the sequences' new tokens),
 `kv_len` int32 [B] (cached tokens, the new ones included), `table` int32
@@ -322,7 +322,8 @@ def qattn_paged_attention(q: torch.Tensor, cache: PagedKVCache, table: torch.Ten
                           stream=None) -> torch.Tensor:
     """Attention of the new tokens' q fp16 [T, Hq, d] over the cache, which holds their keys and values already:
     each sees the cached tokens up to its own position.  `max_new`: an upper bound of the sequences' new tokens
-    where the caller has one (1 for a decode step); it only picks kernels.  `scale` defaults to 1 / sqrt(d)."""
+    where the caller has one (1 for a decode step); it only picks kernels, and a decode step without it takes half as
+    long again.  `scale` defaults to 1 / sqrt(d)."""
     dev = _device(q, "q")
     pq, ldq = _heads(q, "q", dev)
     T, Hq, d = q.shape

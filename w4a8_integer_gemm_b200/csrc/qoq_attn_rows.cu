@@ -46,9 +46,10 @@
 // time switching.  Without the joining in the CTA: 88 against 78.)
 //
 // Measured: those 64 sequences (307 MB of cache, 8 heads of 128 in 4 bits)
-// 78 us, 3.9 TB/s; three of 10^5 tokens in 8 bits (457 MB) 96 us, 4.8 TB/s.
-// What is left is the instructions per token: 20 to 25 per granule and lane
-// to bring and mask the codes, and as many MMAs.
+// 85 us, 3.6 TB/s (80 with two digits of q); two of about 115,000 tokens in 8
+// bits (457 MB) 96 us, 4.8 TB/s.  No pipe is full (issue slots 58%, ALU 50%,
+// HBM 46% in the first): 16 warps of an SM do not hide the latencies of a
+// granule's chain, from codes through scores and weights to values.
 #include <cuda_fp16.h>
 
 #include <cmath>

@@ -36,16 +36,22 @@
 //
 // Bound: for each row tile a step is a chain, softmax (about 1300 cycles of
 // its 16 warps' exponentials and conversions, 900 of waits and stores) and
-// then 1060 cycles of MMAs, which run one after the other because P lies over
-// S and tensor memory has no room for a second S beside O; two row tiles fill
-// a period of 3340 cycles (a cache: 3900) with 2080 of MMAs.  Measured: a
-// prompt of 8192 tokens, 32 heads of 128: 500 us, 1.1 PFLOP/s, 66% of cuBLAS;
-// prompts of 1 to 1800 tokens, 16 heads: 153 us.
+// then 1060 cycles of MMAs, one after the other: P lies over the first half of
+// S, and the next S, a whole one, waits until P V has read it.  (The other half
+// of S is free as soon as S has been read; half of the next S could be computed
+// there meanwhile, which is not done.)  Two row tiles fill a period of 3340
+// cycles (a cache: 3900) with 2080 of MMAs.  Measured, calls back to back under
+// the power limit: a prompt of 8192 tokens, 32 heads of 128: 568 us, 0.97
+// PFLOP/s, 58% of cuBLAS; prompts of 1 to 1800 tokens, 16 heads: 168 us; three
+// chunks over a cache 257 us.
 //
 // Roundings below FP32: P (FP16, as the tensor core's operand: half a step of
 // each weight; the sum of weights is taken before it, in FP32) and, for a
-// cache, the expanded keys and values (half a step, against a quantisation
-// step of 1/15 or 1/255 of the row's range).
+// cache, the expanded keys and values: half a step, what they have in FP16
+// anyway, the type that they were cached from.  (Keys that are not rounded were
+// built in three forms, error 3.4e-4 instead of 7.7e-4 in the norm: two FP16
+// parts of each key 376 to 450 us for chunks that take 257; their codes, with
+// scales and offsets in the softmax, 303 us, and 351 on fragments of S.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 
