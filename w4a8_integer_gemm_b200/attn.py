@@ -201,6 +201,8 @@ class PagedKVCache:
     v_par: torch.Tensor
     bits: int               # 4 or 8
 
+    _made = None            # (no field: what _args was made from; a handle that was pickled without it checks itself)
+
     def __post_init__(self):
         self._check()
 
